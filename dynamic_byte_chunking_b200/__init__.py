@@ -16,6 +16,15 @@ report):
 * :func:`hnet_route`         cosine router p_t, boundaries, chunk list, EMA;
 * :func:`canon_conv1d`       the encoder's Canon layer (causal depthwise conv, k = 4),
   :func:`chunk_coding_rate_canon` the Canon layer and the coding rate in one call.
+
+Between these stages and the models around them:
+
+* :func:`rms_norm`           s = x + residual, y = s / rms(s) * w;
+* :func:`rms_norm_backward`  its gradients;
+* :func:`rms_norm_i8`        the same norm with an 8-bit output and one scale per row;
+* :func:`quantize_rows_i8`   rows (a weight's output channels, activations) in 8 bits;
+* :func:`matmul_i8`          8-bit product with token and channel scales;
+* :func:`chunk_project_i8`   chunk vectors -> norm -> 8 bits -> projection to the global width.
 """
 from __future__ import annotations
 
@@ -30,6 +39,8 @@ __all__ = [
     "chunk_gather", "chunk_upsample", "chunk_upsample_workspace", "chunk_upsample_noalloc",
     "chunk_upsample_backward", "chunk_upsample_backward_workspace", "chunk_gather_backward",
     "hnet_route", "hnet_route_workspace", "chunk", "canon_conv1d", "chunk_coding_rate_canon",
+    "rms_norm", "rms_norm_i8", "rms_norm_backward", "rms_norm_backward_workspace", "quantize_rows_i8",
+    "matmul_i8", "chunk_project_i8",
     "DBC_F32", "DBC_BF16", "BIN_OFFSET", "BIN_FRACTION", "BIN_ABSOLUTE",
     "ERR_NONFINITE", "ERR_TIMEOUT", "ERR_BOUNDS",
 ]
@@ -73,6 +84,15 @@ _SIGS = {
                                        _vp, _vp]),
     "hnet_route": (_int, [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _f32, _int, _vp, _vp, _vp, _vp,
                           _vp, _vp, _sz, _vp, _vp]),
+    "rms_norm": (_int, [_vp, _i64, _int, _vp, _i64, _vp, _int, _i64, _i64, _f32, _vp, _i64, _vp, _i64, _int, _vp,
+                        _vp]),
+    "rms_norm_i8": (_int, [_vp, _i64, _int, _vp, _i64, _vp, _int, _i64, _i64, _f32, _vp, _i64, _vp, _i64, _vp, _vp,
+                           _vp]),
+    "quantize_rows_i8": (_int, [_vp, _i64, _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "rms_norm_backward_workspace": (_sz, [_i64, _i64]),
+    "rms_norm_backward": (_int, [_vp, _i64, _int, _vp, _i64, _int, _vp, _int, _vp, _i64, _i64, _i64, _f32, _vp,
+                                 _i64, _vp, _vp, _sz, _vp, _vp]),
+    "matmul_i8": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _vp]),
 }
 
 
@@ -456,3 +476,294 @@ def chunk_coding_rate_canon(H, w, eps2: float, bias=None, *, offsets=None, T: Op
                                        _stream(stream))
     _check("chunk_coding_rate_canon", rc)
     return Hc, dR
+
+
+# ---------------------------------------------------------------- residual norm and 8-bit products
+def _elsewhere(device, stream):
+    """The stream to make current first: a given one, or the tensors' device's when another is current."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        return stream
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.current_stream(device)
+    return None
+
+
+def _one_device(*ts):
+    device = ts[0].device
+    for t in ts:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("dbc kernels take CUDA tensors only (no CPU path)")
+            if t.device != device:
+                raise ValueError(f"tensors on {device} and {t.device}: all have to be on one device")
+    return device
+
+
+def _code(t, what: str) -> int:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return DBC_BF16
+    if t.dtype == torch.float32:
+        return DBC_F32
+    raise TypeError(f"{what} must be bfloat16 or float32")
+
+
+def _status_word(t):
+    torch = _torch()
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+        raise TypeError("dev_status must be an int32 tensor")
+    return _ptr(t)
+
+
+def _rows_in(t, d: int):
+    """(t2, stride): t as [N, d] rows with unit inner stride; a view where its strides allow, else a copy."""
+    if t.dim() != 2:
+        t = t.reshape(-1, d)
+    N = t.shape[0]
+    if (d > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < d):
+        t = t.contiguous()
+    return t, (t.stride(0) if N > 1 else d)
+
+
+def _rows_out(t, shape, dtype, what: str):
+    """Row stride of a caller's output buffer (its rows are written in place, so it must be a plain one)."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}")
+    d = shape[-1]
+    if t.dim() != 2 and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous, or [N, d] with unit inner stride")
+    N = t.shape[0] if t.dim() == 2 else 1
+    if t.dim() == 2 and ((d > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < d)):
+        raise ValueError(f"{what} must have unit inner stride and a row stride of at least d")
+    return t.stride(0) if t.dim() == 2 and N > 1 else d
+
+
+def _weight_arg(weight, d: int):
+    """(pointer, dtype code, the tensor that holds it)."""
+    if weight is None:
+        return None, DBC_F32, None
+    if weight.dim() != 1 or weight.shape[0] != d:
+        raise ValueError(f"weight must have shape [{d}]")
+    code = _code(weight, "weight")
+    weight = weight.contiguous()
+    return _ptr(weight), code, weight
+
+
+def _norm_inputs(x, residual, weight):
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., d] with d >= 1")
+    d = x.shape[-1]
+    code = _code(x, "x")
+    x2, xs = _rows_in(x, d)
+    r2, rs = None, 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have x's shape and dtype")
+        r2, rs = _rows_in(residual, d)
+    return d, code, x2, xs, r2, rs, _weight_arg(weight, d)
+
+
+def _sum_out(x, residual, s):
+    torch = _torch()
+    if residual is None:
+        if s is not None:
+            raise ValueError("s is the sum x + residual: pass it with a residual only")
+        return None, 0
+    if s is None:
+        s = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return s, _rows_out(s, x.shape, x.dtype, "s")
+
+
+def _codes_out(x, d: int, q, scale):
+    """(q [..., d] int8, its row stride, scale [...]); a fresh q has rows on 16-byte boundaries."""
+    torch = _torch()
+    lead = tuple(x.shape[:-1])
+    if q is None:
+        ld = (d + 15) // 16 * 16
+        q = torch.empty(*lead, ld, dtype=torch.int8, device=x.device)
+        qs = ld
+        if ld != d:
+            q = q[..., :d]
+    else:
+        qs = _rows_out(q, x.shape, torch.int8, "q")
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+    elif tuple(scale.shape) != lead or scale.dtype != torch.float32 or not scale.is_contiguous():
+        raise ValueError(f"scale must be a contiguous float32 tensor of shape {lead}")
+    return q, qs, scale
+
+
+def rms_norm(x, weight=None, *, eps: float = 1e-6, residual=None, out_dtype=None, y=None, s=None, dev_status=None,
+             stream=None):
+    """(y, s): s = x + residual rounded to x's dtype (None without a residual) and y = s / rms(s) * weight
+    in ``out_dtype`` (x's by default), over the last dimension of x [..., d] (fp32 or bf16; weight [d] fp32 or
+    bf16, or None for ones).  ``s`` may be x or residual themselves, ``y`` may be x: updated in place."""
+    torch = _torch()
+    device = _one_device(x, weight, residual, y, s, dev_status)
+    to = _elsewhere(device, stream)
+    if to is not None:
+        with torch.cuda.stream(to):
+            return rms_norm(x, weight, eps=eps, residual=residual, out_dtype=out_dtype, y=y, s=s,
+                            dev_status=dev_status)
+    d, code, x2, xs, r2, rs, (wp, wc, _w) = _norm_inputs(x, residual, weight)
+    s, ss = _sum_out(x, residual, s)
+    if y is None:
+        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=device)
+    ys = _rows_out(y, x.shape, out_dtype or y.dtype, "y")
+    rc = lib().rms_norm(_ptr(x2), xs, code, _ptr(r2), rs, wp, wc, x2.shape[0], d, float(eps), _ptr(s), ss, _ptr(y),
+                        ys, _code(y, "y"), _status_word(dev_status), _stream(None))
+    _check("rms_norm", rc)
+    return y, s
+
+
+def rms_norm_i8(x, weight=None, *, eps: float = 1e-6, residual=None, q=None, scale=None, s=None, dev_status=None,
+                stream=None):
+    """(q, scale, s): rms_norm with an int8 output q [..., d] and one fp32 scale per row, q * scale standing
+    for y; s as in :func:`rms_norm`.  A fresh q has its rows on 16-byte boundaries (it is a view when d is not a
+    multiple of 16), as :func:`matmul_i8` reads them."""
+    torch = _torch()
+    device = _one_device(x, weight, residual, q, scale, s, dev_status)
+    to = _elsewhere(device, stream)
+    if to is not None:
+        with torch.cuda.stream(to):
+            return rms_norm_i8(x, weight, eps=eps, residual=residual, q=q, scale=scale, s=s, dev_status=dev_status)
+    d, code, x2, xs, r2, rs, (wp, wc, _w) = _norm_inputs(x, residual, weight)
+    s, ss = _sum_out(x, residual, s)
+    q, qs, scale = _codes_out(x, d, q, scale)
+    rc = lib().rms_norm_i8(_ptr(x2), xs, code, _ptr(r2), rs, wp, wc, x2.shape[0], d, float(eps), _ptr(s), ss,
+                           _ptr(q), qs, _ptr(scale), _status_word(dev_status), _stream(None))
+    _check("rms_norm_i8", rc)
+    return q, scale, s
+
+
+def quantize_rows_i8(x, *, q=None, scale=None, dev_status=None, stream=None):
+    """(q, scale): the rows of x [..., d] (fp32 or bf16) in int8 with one fp32 scale each, q * scale standing
+    for x.  A weight for :func:`matmul_i8` has its output channels as rows: ``quantize_rows_i8(W.t())``."""
+    torch = _torch()
+    device = _one_device(x, q, scale, dev_status)
+    to = _elsewhere(device, stream)
+    if to is not None:
+        with torch.cuda.stream(to):
+            return quantize_rows_i8(x, q=q, scale=scale, dev_status=dev_status)
+    d, code, x2, xs, _r, _rs, _wt = _norm_inputs(x, None, None)
+    q, qs, scale = _codes_out(x, d, q, scale)
+    rc = lib().quantize_rows_i8(_ptr(x2), xs, code, x2.shape[0], d, _ptr(q), qs, _ptr(scale),
+                                _status_word(dev_status), _stream(None))
+    _check("quantize_rows_i8", rc)
+    return q, scale
+
+
+def rms_norm_backward_workspace(N: int, d: int) -> int:
+    return int(lib().rms_norm_backward_workspace(N, d))
+
+
+def rms_norm_backward(dy, s, weight=None, *, eps: float = 1e-6, dsum=None, want_dw: bool = True, dx=None, dw=None,
+                      workspace=None, dev_status=None, stream=None):
+    """(dx, dw): gradients of :func:`rms_norm` from dy [..., d] (fp32 or bf16) and the normalised sum s (x
+    itself when there was no residual).  ``dsum`` is the gradient that reaches s from elsewhere; dx (s's dtype) is
+    the gradient of x and of the residual alike; dw is fp32 [d], or None when ``want_dw`` is False."""
+    torch = _torch()
+    device = _one_device(dy, s, weight, dsum, dx, dw, workspace, dev_status)
+    to = _elsewhere(device, stream)
+    if to is not None:
+        with torch.cuda.stream(to):
+            return rms_norm_backward(dy, s, weight, eps=eps, dsum=dsum, want_dw=want_dw, dx=dx, dw=dw,
+                                     workspace=workspace, dev_status=dev_status)
+    d, code, s2, ss, g2, gs, (wp, wc, _w) = _norm_inputs(s, dsum, weight)
+    if dy.shape != s.shape:
+        raise ValueError("dy must have the shape of s")
+    dyc = _code(dy, "dy")
+    dy2, ys = _rows_in(dy, d)
+    N = s2.shape[0]
+    if dx is None:
+        dx = torch.empty(s.shape, dtype=s.dtype, device=device)
+    xs = _rows_out(dx, s.shape, s.dtype, "dx")
+    ws = None
+    if want_dw:
+        if dw is None:
+            dw = torch.empty(d, dtype=torch.float32, device=device)
+        elif tuple(dw.shape) != (d,) or dw.dtype != torch.float32 or not dw.is_contiguous():
+            raise ValueError(f"dw must be a contiguous float32 tensor of shape ({d},)")
+        ws = _workspace(rms_norm_backward_workspace(N, d), device, workspace)
+    elif dw is not None:
+        raise ValueError("dw was given with want_dw=False")
+    rc = lib().rms_norm_backward(_ptr(dy2), ys, dyc, _ptr(s2), ss, code, wp, wc, _ptr(g2), gs, N, d, float(eps),
+                                 _ptr(dx), xs, _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel(),
+                                 _status_word(dev_status), _stream(None))
+    _check("rms_norm_backward", rc)
+    return dx, dw
+
+
+def _operand_i8(t, what: str):
+    """(t, stride): int8 rows on 16-byte boundaries; a padded copy where t's are not."""
+    torch = _torch()
+    if t.dim() != 2 or t.dtype != torch.int8:
+        raise TypeError(f"{what} must be a 2-D int8 tensor")
+    R, K = t.shape
+    ld = t.stride(0) if R > 1 else (K + 15) // 16 * 16
+    if (K > 1 and t.stride(1) != 1) or ld < K or ld % 16 or t.data_ptr() % 16:
+        ld = (K + 15) // 16 * 16
+        c = torch.zeros(R, ld, dtype=torch.int8, device=t.device)
+        c[:, :K] = t
+        t = c[:, :K]
+    return t, max(ld, 16)
+
+
+def _scales(t, n: int, what: str):
+    torch = _torch()
+    if tuple(t.shape) != (n,) or t.dtype != torch.float32:
+        raise ValueError(f"{what} must be a float32 tensor of shape ({n},)")
+    return t.contiguous()
+
+
+def matmul_i8(a, a_scale, b, b_scale, *, bias=None, out_dtype=None, out=None, dev_status=None, stream=None):
+    """out [M, N] = a_scale[:, None] * b_scale * (a b^T) (+ bias) of int8 a [M, K] and b [N, K] (rows = output
+    channels), with exact integer sums; ``out_dtype`` bfloat16 (default) or float32; bias [N] fp32 or bf16.
+    Rows that do not start on 16-byte boundaries are copied first; the outputs of :func:`rms_norm_i8` and
+    :func:`quantize_rows_i8` do."""
+    torch = _torch()
+    device = _one_device(a, a_scale, b, b_scale, bias, out, dev_status)
+    to = _elsewhere(device, stream)
+    if to is not None:
+        with torch.cuda.stream(to):
+            return matmul_i8(a, a_scale, b, b_scale, bias=bias, out_dtype=out_dtype, out=out, dev_status=dev_status)
+    a2, lda = _operand_i8(a, "a")
+    b2, ldb = _operand_i8(b, "b")
+    M, K = a2.shape
+    N = b2.shape[0]
+    if b2.shape[1] != K:
+        raise ValueError(f"a has {K} columns and b {b2.shape[1]}")
+    a_scale, b_scale = _scales(a_scale, M, "a_scale"), _scales(b_scale, N, "b_scale")
+    bc = DBC_F32
+    if bias is not None:
+        if tuple(bias.shape) != (N,):
+            raise ValueError(f"bias must have shape ({N},)")
+        bc = _code(bias, "bias")
+        bias = bias.contiguous()
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=device)
+    ldo = _rows_out(out, (M, N), out_dtype or out.dtype, "out")
+    rc = lib().matmul_i8(_ptr(a2), lda, _ptr(a_scale), _ptr(b2), ldb, _ptr(b_scale), _ptr(bias), bc, M, N, K,
+                         _ptr(out), ldo, _code(out, "out"), _status_word(dev_status), _stream(None))
+    _check("matmul_i8", rc)
+    return out
+
+
+def chunk_project_i8(H, idx, idx_offsets, weight, W_q, W_scale, *, rows: int, T: int, offsets=None,
+                     total: Optional[int] = None, eps: float = 1e-6, bias=None, out_dtype=None, dev_status=None,
+                     stream=None):
+    """Chunk vectors to the global width in 8 bits: (Z, out) with Z = H[s_k] (:func:`chunk_gather`) and
+    out = bf16(rms_norm(Z, weight) W) through :func:`rms_norm_i8` and :func:`matmul_i8`.  ``W_q`` int8 [d_g, d]
+    and ``W_scale`` fp32 [d_g] come from ``quantize_rows_i8(W_proj.t())``, once."""
+    torch = _torch()
+    to = _elsewhere(_one_device(H, idx, idx_offsets, weight, W_q, W_scale, offsets, bias, dev_status), stream)
+    if to is not None:
+        with torch.cuda.stream(to):
+            return chunk_project_i8(H, idx, idx_offsets, weight, W_q, W_scale, rows=rows, T=T, offsets=offsets,
+                                    total=total, eps=eps, bias=bias, out_dtype=out_dtype, dev_status=dev_status)
+    Z = chunk_gather(H, idx, idx_offsets, rows=rows, T=T, offsets=offsets, total=total, dev_status=dev_status)
+    q, scale, _ = rms_norm_i8(Z, weight, eps=eps, dev_status=dev_status)
+    return Z, matmul_i8(q, scale, W_q, W_scale, bias=bias, out_dtype=out_dtype, dev_status=dev_status)

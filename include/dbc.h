@@ -8,7 +8,10 @@
  *     optional local->global projection) and the 16-bin multi-linear upsampler
  *     with its residual;
  *   - an H-Net style cosine-similarity router with EMA smoothing, as a second
- *     boundary rule (ByteGen analysis report, "H-Net architecture").
+ *     boundary rule (ByteGen analysis report, "H-Net architecture");
+ *   - what stands between those stages and the models around them: the RMS norm
+ *     of the residual stream (with its backward pass and an 8-bit output), row
+ *     quantisation and the 8-bit matrix product with token and channel scales.
  *
  * Conventions shared by every entry point
  *   - All pointers named H, dR, idx, Z, S, p, ... are DEVICE pointers owned by
@@ -385,6 +388,118 @@ DBC_API dbc_status hnet_route(const void *H, const int64_t *offsets, int64_t row
                       int64_t *chunk_idx, int64_t *chunk_offsets, float *z_smooth,
                       void *ws, size_t ws_bytes, int32_t *dev_status,
                       dbc_stream_t stream);
+
+/* -------------------------------------------------------------------------
+ * rms_norm -- root-mean-square norm of the residual stream.
+ *
+ * Pre-norm layers around the chunker (local encoder, global model, local
+ * decoder) add a branch to the residual stream and normalise the sum:
+ *   s = T(x + residual)      rounded once to x's type (s = x without residual),
+ *   y = s * rstd * w,        rstd = 1 / sqrt(mean(s^2) + eps).
+ * The stored sum is what is normalised, so rms_norm_backward needs only s.
+ * Squares that leave fp32's range are summed in fp64.
+ *
+ * x        [N, d] fp32 or bf16 (dtype), row r at x + r * x_stride elements.
+ * residual NULL or [N, d] of the same type, r_stride.
+ * weight   NULL (ones) or [d], fp32 or bf16 (w_dtype).
+ * s        out [N, d] of x's type, s_stride; NULL when the sum is not needed;
+ *          must be NULL without residual.  May be x or residual themselves.
+ * y        out [N, d] fp32 or bf16 (y_dtype), y_stride.  May be x itself, and
+ *          residual when s is neither, given equal types and strides.  Other
+ *          overlaps of inputs and outputs are not allowed.
+ * All strides are in elements, >= d.  Any d from 1 to 16384; 16-byte accesses
+ * when d is a multiple of 8 and every row starts on a 16-byte boundary.
+ * A row with a NaN gives NaN, one with an infinity 0 and NaN at the infinity;
+ * both flag NONFINITE.
+ * Errors: INVALID_ARG (NULL/negative/stride < d/eps not finite and > 0/a
+ * pointer off its type's alignment), UNSUPPORTED (dtype, d > 16384), CUDA;
+ * device flag NONFINITE.
+ * ------------------------------------------------------------------------- */
+DBC_API dbc_status rms_norm(const void *x, int64_t x_stride, int dtype, const void *residual, int64_t r_stride,
+                            const void *weight, int w_dtype, int64_t N, int64_t d, float eps, void *s,
+                            int64_t s_stride, void *y, int64_t y_stride, int y_dtype, int32_t *dev_status,
+                            dbc_stream_t stream);
+
+/* -------------------------------------------------------------------------
+ * rms_norm_i8 -- rms_norm with an 8-bit output and one scale per row.
+ *
+ *   p = fp32(s * w), m = max |p| over the row,
+ *   q = rint(127 p / m)  (in [-127, 127], halves to even, decided exactly),
+ *   scale = m * rstd / 127,  so that q * scale stands for y.
+ * rstd does not enter q.  A row with m = 0 gives q = 0, scale = 0; a row in
+ * which s or p is not finite gives q = 0, scale = NaN and flags NONFINITE.
+ *
+ * q        out int8 [N, d], q_stride >= d bytes; bytes between the rows are
+ *          left as they were.  A q_stride that is a multiple of 16 makes q an
+ *          operand of matmul_i8.
+ * scale    out fp32 [N].
+ * The other arguments, limits and errors are rms_norm's.
+ * ------------------------------------------------------------------------- */
+DBC_API dbc_status rms_norm_i8(const void *x, int64_t x_stride, int dtype, const void *residual, int64_t r_stride,
+                               const void *weight, int w_dtype, int64_t N, int64_t d, float eps, void *s,
+                               int64_t s_stride, int8_t *q, int64_t q_stride, float *scale, int32_t *dev_status,
+                               dbc_stream_t stream);
+
+/* -------------------------------------------------------------------------
+ * quantize_rows_i8 -- rows in 8 bits with one scale each.
+ *
+ *   m = max |x| over the row, q = rint(127 x / m) (halves to even, decided
+ *   exactly), scale = m / 127.
+ * For a weight whose rows are output channels, and for activations that have
+ * no norm in front.  Zero and non-finite rows as in rms_norm_i8.
+ * x, q, scale, limits and errors as in rms_norm_i8.
+ * ------------------------------------------------------------------------- */
+DBC_API dbc_status quantize_rows_i8(const void *x, int64_t x_stride, int dtype, int64_t N, int64_t d, int8_t *q,
+                                    int64_t q_stride, float *scale, int32_t *dev_status, dbc_stream_t stream);
+
+/* -------------------------------------------------------------------------
+ * rms_norm_backward -- gradients of rms_norm.
+ *
+ * With g = dy * w and xhat = s * rstd (rstd recomputed from s):
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + ds,   dw = sum over rows of dy * xhat.
+ * dx is the gradient of x and, equally, of the residual; ds is the gradient
+ * that reaches the stored sum from elsewhere (the residual stream).
+ *
+ * dy       [N, d] fp32 or bf16 (dy_dtype), dy_stride.
+ * s        [N, d] (dtype): rms_norm's s, or its x when there was no residual.
+ * ds       NULL or [N, d] (dtype), ds_stride.
+ * dx       out [N, d] (dtype), dx_stride; may be s or ds themselves (equal
+ *          strides), or dy when the types are equal too.
+ * dw       out fp32 [d] (overwritten), or NULL when it is not needed.
+ * ws       workspace of rms_norm_backward_workspace(N, d) bytes; not read when
+ *          dw is NULL.  Calls that can overlap need workspaces of their own.
+ * dw is summed in a fixed order: repeated calls agree bitwise.
+ * Limits and errors as in rms_norm, and WORKSPACE.
+ * ------------------------------------------------------------------------- */
+DBC_API size_t rms_norm_backward_workspace(int64_t N, int64_t d);
+DBC_API dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int dy_dtype, const void *s,
+                                     int64_t s_stride, int dtype, const void *weight, int w_dtype, const void *ds,
+                                     int64_t ds_stride, int64_t N, int64_t d, float eps, void *dx,
+                                     int64_t dx_stride, float *dw, void *ws, size_t ws_bytes, int32_t *dev_status,
+                                     dbc_stream_t stream);
+
+/* -------------------------------------------------------------------------
+ * matmul_i8 -- product of 8-bit integers with token and channel scales.
+ *
+ *   out[i, j] = T(a_scale[i] * b_scale[j] * sum_k a[i, k] b[j, k] (+ bias[j])),
+ * the sum exact in 32-bit integers, the rest in fp32, rounded once.
+ *
+ * a        int8 [M, K], row i at a + i * lda; b int8 [N, K], row j (an output
+ *          channel) at b + j * ldb.  lda, ldb multiples of 16, >= K, both bases
+ *          16-byte aligned; bytes behind a row's K are not used.
+ * a_scale  fp32 [M]; b_scale fp32 [N]; bias NULL or [N], fp32 or bf16
+ *          (bias_dtype).
+ * out      [M, N] fp32 or bf16 (out_dtype), row i at out + i * ldo elements,
+ *          ldo >= N; must not overlap an input.
+ * Any M, N >= 0; 0 <= K <= 131071 (no sum leaves 32 bits; K = 0 leaves the
+ * bias or zeros).  M, N up to 2^31 - 1024.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtypes, K or M, N above the limits), CUDA;
+ * device flag TIMEOUT.
+ * ------------------------------------------------------------------------- */
+DBC_API dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_scale, const int8_t *b, int64_t ldb,
+                             const float *b_scale, const void *bias, int bias_dtype, int64_t M, int64_t N,
+                             int64_t K, void *out, int64_t ldo, int out_dtype, int32_t *dev_status,
+                             dbc_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,414 @@
+"""GPU parity of rms_norm, rms_norm_i8, quantize_rows_i8 and rms_norm_backward against the float64 oracle, with
+the elementwise bounds that oracle/norm.py derives; 8-bit codes have to be equal."""
+import numpy as np
+import pytest
+
+from oracle import norm as o
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+# one thread, tiles and their edges, odd widths, every width class up to the limit
+WIDTHS = [1, 2, 7, 8, 31, 64, 72, 100, 128, 136, 255, 256, 257, 264, 512, 520, 1000, 1024, 1032, 1536, 2048, 2056,
+          2600, 4096, 4104, 5001, 8192, 8200, 16376, 16383, 16384]
+
+
+def _rows(d):
+    """Row counts: a few for wide rows, enough for several blocks for narrow ones."""
+    return [1, 3, 37] if d > 2048 else [1, 2, 5, 333]
+
+
+def _t(v, T, dev="cuda"):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(v)).to(dev).to(torch.bfloat16 if T == "bf16" else torch.float32)
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _vals(rng, shape, T):
+    return o.store(rng.standard_normal(shape).astype(np.float32), T)
+
+
+def _weight(rng, d, T):
+    return o.store((1 + 0.2 * rng.standard_normal(d)).astype(np.float32), T)
+
+
+def _close(got, ref, bound, what):
+    got = _np(got)
+    assert got.shape == ref.shape, what
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.max(np.abs(got - ref) / bound):.2f} bounds"
+
+
+def _status():
+    import torch
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+def test_rms_norm(d):
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    rng = np.random.default_rng(d)
+    st = _status()
+    for k, N in enumerate(_rows(d)):
+        for T, TY, res in (("bf16", "bf16", True), ("f32", "bf16", k % 2 == 0), ("bf16", "f32", False), ("f32", "f32", True)):
+            x = _vals(rng, (N, d), T)
+            r = _vals(rng, (N, d), T) if res else None
+            w = _weight(rng, d, "bf16" if k % 2 else "f32") if d % 3 else None
+            s = o.residual_sum(x, r, T)
+            y, sg = dbc.rms_norm(_t(x, T), None if w is None else _t(w, "bf16" if k % 2 else "f32"), eps=EPS,
+                                 residual=None if r is None else _t(r, T),
+                                 out_dtype=torch.bfloat16 if TY == "bf16" else torch.float32, dev_status=st)
+            assert (sg is None) == (r is None)
+            if r is not None:
+                assert np.array_equal(_np(sg), s), (N, T)
+            ref = o.rms_norm(s, w, EPS)
+            _close(y, ref, o.rms_norm_bound(ref, TY), f"N={N} {T}->{TY}")
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+def test_rms_norm_i8_and_quantize(d):
+    import dynamic_byte_chunking_b200 as dbc
+    rng = np.random.default_rng(1000 + d)
+    st = _status()
+    for k, N in enumerate(_rows(d)):
+        for T in ("bf16", "f32"):
+            x = _vals(rng, (N, d), T)
+            r = _vals(rng, (N, d), T) if k % 2 == 0 else None
+            w = _weight(rng, d, "bf16") if d % 3 else None
+            s = o.residual_sum(x, r, T)
+            q, sc, sg = dbc.rms_norm_i8(_t(x, T), None if w is None else _t(w, "bf16"), eps=EPS,
+                                        residual=None if r is None else _t(r, T), dev_status=st)
+            qr, sr = o.rms_norm_i8(s, w, EPS)
+            assert np.array_equal(q.cpu().numpy(), qr), (N, T)
+            assert q.stride(0) % 16 == 0 or N == 1
+            _close(sc, sr, np.abs(sr) * (o.CHAIN / 2 + o.OPS) * o.U32, f"scale N={N} {T}")
+            if r is not None:
+                assert np.array_equal(_np(sg), s)
+            q, sc = dbc.quantize_rows_i8(_t(x, T), dev_status=st)
+            qr, sr = o.quantize_rows_i8(x)
+            assert np.array_equal(q.cpu().numpy(), qr), (N, T)
+            _close(sc, sr, np.abs(sr) * 2 * o.U32, f"quantize scale N={N} {T}")
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+def test_rms_norm_backward(d):
+    import dynamic_byte_chunking_b200 as dbc
+    rng = np.random.default_rng(2000 + d)
+    st = _status()
+    for k, N in enumerate(_rows(d)):
+        for TY, T, has in (("bf16", "bf16", True), ("f32", "bf16", False), ("bf16", "f32", False), ("f32", "f32", True)):
+            s, dy = _vals(rng, (N, d), T), _vals(rng, (N, d), TY)
+            ds = _vals(rng, (N, d), T) if has else None
+            w = _weight(rng, d, "bf16") if (d + k) % 3 else None
+            dx, dw = dbc.rms_norm_backward(_t(dy, TY), _t(s, T), None if w is None else _t(w, "bf16"), eps=EPS,
+                                           dsum=None if ds is None else _t(ds, T), dev_status=st)
+            rx, rw = o.rms_norm_backward(dy, s, w, EPS, ds)
+            bx, bw = o.backward_bounds(dy, s, w, EPS, ds, T)
+            _close(dx, rx, bx, f"dx N={N} {TY} {T}")
+            _close(dw, rw, bw, f"dw N={N} {TY} {T}")
+            none, nodw = dbc.rms_norm_backward(_t(dy, TY), _t(s, T), None if w is None else _t(w, "bf16"), eps=EPS,
+                                               dsum=None if ds is None else _t(ds, T), want_dw=False)
+            assert nodw is None and np.array_equal(_np(none), _np(dx))
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("N,d", [(20011, 64), (70001, 256), (9001, 1000), (3001, 4096)])
+def test_many_rows(N, d):
+    """More rows than the grid holds at once; dw from long sums, twice the same bits."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    rng = np.random.default_rng(N)
+    x, r, dy = (_vals(rng, (N, d), "bf16") for _ in range(3))
+    w = _weight(rng, d, "bf16")
+    s = o.residual_sum(x, r, "bf16")
+    xt, rt, dyt, wt = _t(x, "bf16"), _t(r, "bf16"), _t(dy, "bf16"), _t(w, "bf16")
+    y, sg = dbc.rms_norm(xt, wt, eps=EPS, residual=rt)
+    ref = o.rms_norm(s, w, EPS)
+    _close(y, ref, o.rms_norm_bound(ref, "bf16"), "y")
+    assert np.array_equal(_np(sg), s)
+    q, sc, _ = dbc.rms_norm_i8(xt, wt, eps=EPS, residual=rt)
+    qr, sr = o.rms_norm_i8(s, w, EPS)
+    assert np.array_equal(q.cpu().numpy(), qr)
+    dx, dw = dbc.rms_norm_backward(dyt, sg, wt, eps=EPS)
+    rx, rw = o.rms_norm_backward(dy, s, w, EPS, None)
+    bx, bw = o.backward_bounds(dy, s, w, EPS, None, "bf16")
+    _close(dx, rx, bx, "dx")
+    _close(dw, rw, bw, "dw")
+    again = dbc.rms_norm_backward(dyt, sg, wt, eps=EPS)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+@pytest.mark.parametrize("T", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [40, 256, 1000, 2048])
+def test_extreme_rows(T, d):
+    """Zero rows, rows whose squares overflow or vanish in fp32, tiny maxima, exact halves under the code."""
+    import dynamic_byte_chunking_b200 as dbc
+    rng = np.random.default_rng(d)
+    base = _vals(rng, (8, d), T)
+    x = base.copy()
+    x[0] = 0
+    x[1] = o.store(base[1] * 2.0 ** 100, T)       # squares overflow
+    x[2] = o.store(base[2] * 2.0 ** -90, T)       # squares vanish
+    x[3] = o.store(base[3] * 2.0 ** -128, T)      # subnormal values
+    x[4] = 0
+    x[4, -1] = o.store(np.array(-3e38), T)
+    x[5] = np.arange(d) % 128 - 0.5               # halves: p = j + 1/2 under a maximum of 127
+    x[5, 0] = 127
+    x[6] = -x[5]
+    st = _status()
+    w = o.store(2.0 ** rng.integers(-1, 1, d), T)
+    for eps in (EPS, 1e-30):
+        y, _ = dbc.rms_norm(_t(x, T), _t(w, T), eps=eps, dev_status=st)
+        ref = o.rms_norm(x, w, eps)
+        _close(y, ref, o.rms_norm_bound(ref, T), f"eps={eps}")
+        q, sc, _ = dbc.rms_norm_i8(_t(x, T), _t(w, T), eps=eps, dev_status=st)
+        qr, sr = o.rms_norm_i8(x, w, eps)
+        assert np.array_equal(q.cpu().numpy(), qr)
+        _close(sc, sr, np.abs(sr) * (o.CHAIN / 2 + o.OPS) * o.U32 + o.TINY["f32"], "scale")
+        dy = _vals(rng, (8, d), T)
+        dx, _ = dbc.rms_norm_backward(_t(dy, T), _t(x, T), _t(w, T), eps=eps, want_dw=False, dev_status=st)
+        rx, _ = o.rms_norm_backward(dy, x, w, eps, None)
+        bx, _ = o.backward_bounds(dy, x, w, eps, None, T)
+        with np.errstate(over="ignore"):
+            rx32 = rx.astype(np.float32)
+        keep = np.isfinite(rx32)                   # a gradient above the type's range becomes an infinity
+        got = _np(dx)
+        assert np.all(np.abs(got - rx)[keep] <= bx[keep])
+    q, sc = dbc.quantize_rows_i8(_t(x, T), dev_status=st)
+    qr, sr = o.quantize_rows_i8(x)
+    assert np.array_equal(q.cpu().numpy(), qr)
+    _close(sc, sr, np.abs(sr) * 2 * o.U32 + o.TINY["f32"], "quantize scale")
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("d", [33, 256, 1536, 6000])
+@pytest.mark.parametrize("T", ["bf16", "f32"])
+def test_non_finite_rows_stay_alone(T, d):
+    import dynamic_byte_chunking_b200 as dbc
+    rng = np.random.default_rng(d)
+    x = _vals(rng, (7, d), T)
+    clean = x.copy()
+    x[2, d // 2] = np.nan
+    x[4, 0] = np.inf
+    x[5, -1] = -np.inf
+    x[5, 0] = np.nan
+    good = [0, 1, 3, 6]
+    st = _status()
+    y, _ = dbc.rms_norm(_t(x, T), None, eps=EPS, dev_status=st)
+    assert st.item() == 1 << dbc.ERR_NONFINITE
+    yc, _ = dbc.rms_norm(_t(clean, T), None, eps=EPS)
+    y, yc = _np(y), _np(yc)
+    assert np.array_equal(y[good], yc[good])
+    assert np.isnan(y[2]).all() and np.isnan(y[5]).all() and np.isnan(y[4, 0]) and not y[4, 1:].any()
+    for call in (lambda s_: dbc.rms_norm_i8(_t(x, T), None, eps=EPS, dev_status=s_)[:2],
+                 lambda s_: dbc.quantize_rows_i8(_t(x, T), dev_status=s_)):
+        st = _status()
+        q, sc = call(st)
+        assert st.item() == 1 << dbc.ERR_NONFINITE
+        q, sc = q.cpu().numpy(), _np(sc)
+        assert not q[[2, 4, 5]].any() and np.isnan(sc[[2, 4, 5]]).all()
+        assert np.isfinite(sc[good]).all() and np.array_equal(q[good], o.quantize_rows_i8(clean)[0][good])
+    st = _status()
+    dx, _ = dbc.rms_norm_backward(_t(clean, T), _t(x, T), None, eps=EPS, want_dw=False, dev_status=st)
+    assert st.item() == 1 << dbc.ERR_NONFINITE
+    dc, _ = dbc.rms_norm_backward(_t(clean, T), _t(clean, T), None, eps=EPS, want_dw=False)
+    assert np.array_equal(_np(dx)[good], _np(dc)[good])
+
+
+@pytest.mark.parametrize("T", ["bf16", "f32"])
+@pytest.mark.parametrize("d,pad,shift", [(256, 64, 0), (256, 8, 8), (256, 3, 1), (1024, 1, 0), (100, 28, 5), (31, 1, 1),
+                                         (4096, 24, 8), (2051, 2, 1)])
+def test_strided_and_unaligned_rows(T, d, pad, shift):
+    """Rows inside wider buffers, some off the 16-byte grid: same results, neighbours untouched."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    rng = np.random.default_rng(d + pad)
+    N, ld = 9, d + pad + shift
+    dt = torch.bfloat16 if T == "bf16" else torch.float32
+
+    def inside(v):
+        buf = torch.full((N, ld), 7.0, dtype=dt, device="cuda")
+        view = buf[:, shift:shift + d]
+        if v is not None:
+            view.copy_(_t(v, T))
+        return buf, view
+
+    def kept(buf):
+        b = buf.clone()
+        b[:, shift:shift + d] = 7.0
+        return bool((b == 7.0).all())
+
+    x, r, dy, ds = (_vals(rng, (N, d), T) for _ in range(4))
+    w = _weight(rng, d, T)
+    xv, rv, dyv, dsv = (inside(v)[1] for v in (x, r, dy, ds))
+    (sb, s), (yb, y), (xb, dx) = inside(None), inside(None), inside(None)
+    dbc.rms_norm(xv, _t(w, T), eps=EPS, residual=rv, y=y, s=s)
+    yr, sr = dbc.rms_norm(_t(x, T), _t(w, T), eps=EPS, residual=_t(r, T))
+    assert torch.equal(s, sr) and kept(sb) and kept(yb)
+    ref = o.rms_norm(o.residual_sum(x, r, T), w, EPS)
+    _close(y, ref, o.rms_norm_bound(ref, T), "y")
+    dbc.rms_norm_backward(dyv, s, _t(w, T), eps=EPS, dsum=dsv, dx=dx)
+    rx, _ = o.rms_norm_backward(dy, _np(sr), w, EPS, ds)
+    bx, _ = o.backward_bounds(dy, _np(sr), w, EPS, ds, T)
+    _close(dx, rx, bx, "dx")
+    assert kept(xb)
+    qb = torch.full((N, ld), 99, dtype=torch.int8, device="cuda")
+    q, sc, _ = dbc.rms_norm_i8(xv, _t(w, T), eps=EPS, residual=rv, q=qb[:, shift:shift + d])
+    qr, _, _ = dbc.rms_norm_i8(_t(x, T), _t(w, T), eps=EPS, residual=_t(r, T))
+    assert torch.equal(q, qr)
+    qb[:, shift:shift + d] = 99
+    assert bool((qb == 99).all())
+    # a transposed and a broadcast input are copied first
+    xt = _t(x, T).t().contiguous().t()
+    one = _t(r[:1], T).expand(N, d)
+    y2, s2 = dbc.rms_norm(xt, _t(w, T), eps=EPS, residual=one)
+    y3, s3 = dbc.rms_norm(_t(x, T), _t(w, T), eps=EPS, residual=one.contiguous())
+    assert torch.equal(y2, y3) and torch.equal(s2, s3)
+
+
+@pytest.mark.parametrize("d", [96, 256, 257, 1536, 8192])
+def test_in_place_forms(d):
+    """s over residual or x, y over x, dx over s, dsum or dy."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    rng = np.random.default_rng(d)
+    N = 301
+    x, r, w = _t(_vals(rng, (N, d), "bf16"), "bf16"), _t(_vals(rng, (N, d), "bf16"), "bf16"), _t(_weight(rng, d, "bf16"), "bf16")
+    y, s = dbc.rms_norm(x, w, eps=EPS, residual=r)
+    r2, x2 = r.clone(), x.clone()
+    y2, _ = dbc.rms_norm(x2, w, eps=EPS, residual=r2, s=r2, y=x2)
+    assert torch.equal(y2, y) and torch.equal(r2, s) and y2 is x2
+    x3 = x.clone()
+    y3, _ = dbc.rms_norm(x3, w, eps=EPS, residual=r, s=x3)
+    assert torch.equal(y3, y) and torch.equal(x3, s)
+    q, sc, _ = dbc.rms_norm_i8(x, w, eps=EPS, residual=r)
+    r4 = r.clone()
+    q4, sc4, _ = dbc.rms_norm_i8(x, w, eps=EPS, residual=r4, s=r4)
+    assert torch.equal(q4, q) and torch.equal(sc4, sc) and torch.equal(r4, s)
+    dy, ds = _t(_vals(rng, (N, d), "bf16"), "bf16"), _t(_vals(rng, (N, d), "bf16"), "bf16")
+    dx, dw = dbc.rms_norm_backward(dy, s, w, eps=EPS, dsum=ds)
+    for k in range(3):
+        c = [dy.clone(), s.clone(), ds.clone()]
+        dx2, dw2 = dbc.rms_norm_backward(c[0], c[1], w, eps=EPS, dsum=c[2], dx=c[k])
+        assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
+def test_shapes_and_empty_batches():
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    x = torch.randn(3, 5, 48, device="cuda")
+    y, _ = dbc.rms_norm(x, eps=EPS)
+    q, sc, s = dbc.rms_norm_i8(x, eps=EPS, residual=x)
+    assert y.shape == x.shape and q.shape == x.shape and sc.shape == (3, 5) and s.shape == x.shape
+    one, _ = dbc.rms_norm(x[0, 0], eps=EPS)
+    assert torch.equal(one, y[0, 0])
+    e = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    assert dbc.rms_norm(e)[0].shape == (0, 64) and dbc.quantize_rows_i8(e)[0].shape == (0, 64)
+    dx, dw = dbc.rms_norm_backward(e, e)
+    assert dx.shape == (0, 64) and not dw.any() and dw.shape == (64,)
+
+
+def test_binding_refusals():
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    x = torch.zeros(4, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        dbc.rms_norm(x, torch.ones(63, device="cuda"))
+    with pytest.raises(TypeError):
+        dbc.rms_norm(x, torch.ones(64, device="cuda", dtype=torch.float16))
+    with pytest.raises(TypeError):
+        dbc.rms_norm(x.half())
+    with pytest.raises(ValueError):
+        dbc.rms_norm(x, residual=x.float())
+    with pytest.raises(ValueError):
+        dbc.rms_norm(x, residual=x[:2])
+    with pytest.raises(ValueError):
+        dbc.rms_norm(x, s=x)
+    with pytest.raises(ValueError):
+        dbc.rms_norm(x, y=torch.zeros(64, 4, device="cuda", dtype=torch.bfloat16).t())
+    with pytest.raises(ValueError):
+        dbc.rms_norm(x, y=x.clone(), out_dtype=torch.float32)
+    with pytest.raises(ValueError):
+        dbc.rms_norm(x, torch.ones(64))
+    with pytest.raises(ValueError):
+        dbc.rms_norm_i8(x, scale=torch.zeros(3, device="cuda"))
+    with pytest.raises(ValueError):
+        dbc.rms_norm_backward(x[:2], x)
+    with pytest.raises(ValueError):
+        dbc.rms_norm_backward(x, x, want_dw=False, dw=torch.zeros(64, device="cuda"))
+    with pytest.raises(TypeError):
+        dbc.rms_norm(x, dev_status=torch.zeros(1, device="cuda"))
+    with pytest.raises(dbc.DbcError):
+        dbc.rms_norm(x, eps=0.0)
+    with pytest.raises(dbc.DbcError):
+        dbc.quantize_rows_i8(torch.zeros(1, 16385, device="cuda"))
+
+
+def test_other_stream_and_captured_graphs():
+    """A stream argument orders the copies too; graphs replay on new data, two of them at once."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    torch.manual_seed(0)
+    x, r = torch.randn(2, 700, 512, device="cuda").bfloat16()
+    w = torch.randn(512, device="cuda").bfloat16()
+    y, s = dbc.rms_norm(x, w, residual=r)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y2, s2 = dbc.rms_norm(x.t().contiguous().t(), w, residual=r, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, y2) and torch.equal(s, s2)
+
+    graphs = []
+    for k in range(2):
+        ins = [torch.zeros_like(x), torch.zeros_like(r)]
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            def body():
+                y_, s_ = dbc.rms_norm(ins[0], w, residual=ins[1])
+                q_, c_, _ = dbc.rms_norm_i8(ins[0], w, residual=ins[1])
+                dx_, dw_ = dbc.rms_norm_backward(y_, s_, w, dsum=ins[0])
+                return y_, s_, q_, c_, dx_, dw_
+            body()
+        torch.cuda.current_stream().wait_stream(st)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            outs = body()
+        graphs.append((g, ins, outs, st, body))
+    for trial in range(3):
+        data = [torch.randn(2, 700, 512, device="cuda").bfloat16() for _ in graphs]
+        torch.cuda.synchronize()
+        for (g, ins, outs, st, body), v in zip(graphs, data):
+            with torch.cuda.stream(st):
+                ins[0].copy_(v[0])
+                ins[1].copy_(v[1])
+                g.replay()
+        torch.cuda.synchronize()
+        for (g, ins, outs, st, body), v in zip(graphs, data):
+            for a, b in zip(outs, body()):
+                assert torch.equal(a, b)
+
+
+def test_row_offsets_past_32_bits():
+    """A batch whose last rows lie past 2^31 elements and 2^32 bytes."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    N, d = 8_400_003, 264                          # 2.2e9 elements
+    x = torch.zeros(N, d, dtype=torch.bfloat16, device="cuda")
+    x[-5:] = torch.randn(5, d, device="cuda").bfloat16()
+    tail = x[-5:].clone()
+    y, _ = dbc.rms_norm(x, eps=EPS)
+    assert torch.equal(y[-5:], dbc.rms_norm(tail, eps=EPS)[0]) and not y[:1000].any()
+    dx, dw = dbc.rms_norm_backward(x, x, eps=EPS, dx=y)
+    rx, rw = dbc.rms_norm_backward(tail, tail, eps=EPS)
+    assert torch.equal(dx[-5:], rx)
+    assert torch.allclose(dw, rw, rtol=1e-5, atol=1e-5)
+    del y, dx
+    q, sc = dbc.quantize_rows_i8(x)
+    assert torch.equal(q[-5:], dbc.quantize_rows_i8(tail)[0]) and torch.equal(sc[-5:], dbc.quantize_rows_i8(tail)[1])
