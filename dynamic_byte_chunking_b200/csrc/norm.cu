@@ -1,77 +1,31 @@
 // Residual RMS norm, its 8-bit form, row quantisation and the norm's backward
 // pass (formulas at the declarations in dbc.h).
 //
-// All of it is bound by HBM: a row is read, two row sums or a sum and a
-// maximum are taken, and the row is written.  Sums are fp32; a row whose sum
-// of squares leaves [1e-30, 1e37] (squares that overflow or vanish in fp32) is
-// summed again in fp64 and finished there.
-#include "common.cuh"
+// All of it is bound by HBM.  A row is read once into registers, its sum of
+// squares (and the maximum under the 8-bit code) is reduced over the threads
+// that hold it, and it is written from there.  Sums are fp32; a row whose sum
+// of squares leaves [1e-30, 1e37] (squares that overflow or vanish in fp32, or
+// something not finite) is summed again in fp64 from the registers.
+//
+// Rows of up to 128 fragments (16 bytes each; 512 single elements) belong to a
+// team of 8, 16 or 32 lanes, R rows at a time so that each thread keeps about
+// four loads per input in flight; wider rows belong to a CTA.
+#include "norm.cuh"
 
 namespace dbc {
 namespace nm {
 
 constexpr int kThreads = 256;
 constexpr int64_t kMaxD = 16384;
+constexpr float kLow = 1e-30f, kHigh = 1e37f;
 
+// kI8Narrow: the norm's 8-bit form where s * w has 16 significant bits (bf16
+// rows, bf16 weight or none); kQuant: no norm, p = x.
+enum { kPlain = 0, kI8 = 1, kI8Narrow = 2, kQuant = 3 };
+constexpr bool norms(int mode) { return mode != kQuant; }
+constexpr bool weighs(int mode) { return mode == kI8 || mode == kI8Narrow; }
 template <class T>
-__device__ __forceinline__ float round_to(float v);
-template <>
-__device__ __forceinline__ float round_to<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float round_to<__nv_bfloat16>(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
-
-__device__ __forceinline__ void st_f(float *p, float v) { *p = v; }
-__device__ __forceinline__ void st_f(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
-// An fp32 or bf16 array read element by element; NULL reads as ones.
-struct Weight {
-    const void *p;
-    int bf16;
-    __device__ __forceinline__ float at(int64_t i) const {
-        if (!p) return 1.f;
-        return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
-    }
-};
-
-// The code of p for a row maximum m: rint(127 p / m), halves to even.  The
-// fp32 quotient is off by less than 127 * 2^-23 = 1.6e-5; where that could
-// decide the rounding, fp64 does: 127 p is exact there, and a quotient of two
-// 24-bit numbers that is not a half-integer is at least 2^-34 away from one
-// (|q| <= 127), far more than the division's rounding.
-__device__ __noinline__ int code_exact(float p, float m) { return (int)rint((double)p * 127.0 / (double)m); }
-__device__ __forceinline__ int code(float p, float m, float inv) {
-    const float t = p * inv, r = rintf(t);
-    if (fabsf(fabsf(t - r) - 0.5f) < 4e-5f) return code_exact(p, m);
-    return (int)r;
-}
-
-// How a row is quantised, from m = max |p|: tiny rows are scaled by 2^100
-// (exact) so that 127 / m stays in range.
-struct Quant {
-    float pre, m, inv;
-    bool bad;
-    __device__ __forceinline__ explicit Quant(float m_, bool nonfinite) {
-        bad = nonfinite || !(m_ <= 3.4028234e38f);
-        pre = m_ < 0x1p-60f ? 0x1p100f : 1.f;
-        m = m_ * pre;
-        inv = m > 0.f ? 127.f / m : 0.f;
-    }
-    __device__ __forceinline__ int operator()(float p) const { return bad || m == 0.f ? 0 : code(p * pre, m, inv); }
-};
-
-template <class F>
-__device__ __forceinline__ double block_reduce(double v, F f, double *sm) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sm[0];
-    for (int i = 1; i < kThreads / 32; ++i) v = f(v, sm[i]);
-    return v;
-}
-
-enum { kPlain = 0, kI8 = 1, kQuantOnly = 2 };
+constexpr bool narrow(int mode) { return mode == kI8Narrow || (mode == kQuant && sizeof(T) == 2); }
 
 struct FwdArgs {
     const void *x, *res;
@@ -85,57 +39,202 @@ struct FwdArgs {
     int32_t *st;
 };
 
-// One CTA per row; the row is read twice (the second time from L2).
-template <class T, int MODE>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const FwdArgs a) {
-    __shared__ double sm[kThreads / 32];
-    auto add = [](double u, double v) { return u + v; };
-    auto mx = [](double u, double v) { return fmax(u, v); };
+// What the row's statistics say: the factors of y = (s * pre) * rstd * w (pre
+// is 1 unless rstd would be subnormal) and the 8-bit scale.
+struct RowFactor {
+    float pre, rstd;
+    __device__ __forceinline__ RowFactor(float ss, int d, float eps) : pre(1.f) {
+        rstd = rsqrtf(ss / (float)d + eps);
+    }
+    __device__ __forceinline__ RowFactor(double ss, int d, float eps) {
+        const double r = 1.0 / sqrt(ss / d + (double)eps);
+        pre = r < 0x1p-120 ? 0x1p-16f : 1.f;
+        rstd = (float)(r / (double)pre);
+    }
+};
+
+// One row from registers to memory (s, then y or q), fragment column `col`.
+template <class T, int NE, int MODE, bool RES>
+__device__ __forceinline__ void write_frag(const FwdArgs &a, int64_t r, int col, const Frag<T, NE> &f,
+                                           const float (&w)[NE], const RowFactor &k, const Quant &qn) {
+    if (RES && a.s) f.store(static_cast<T *>(a.s) + r * a.ss + col);
+    if (MODE == kPlain) {
+        float o[NE];
+#pragma unroll
+        for (int i = 0; i < NE; ++i) o[i] = f.at(i) * k.pre * k.rstd * w[i];
+        store_as<NE>(a.y, a.y_bf16, r * a.ys + col, o);
+    } else {
+        float p[NE];
+#pragma unroll
+        for (int i = 0; i < NE; ++i) p[i] = weighs(MODE) ? f.at(i) * w[i] : f.at(i);
+        qn.template store<narrow<T>(MODE), NE>(a.q + r * a.qs + col, p);
+    }
+}
+
+template <int MODE>
+__device__ __forceinline__ float row_scale(const Quant &q, const RowFactor &k) {
+    if (q.bad) return __int_as_float(0x7fc00000);
+    const float m = q.m;
+    if (!norms(MODE)) return m / 127.f;
+    // the order that leaves fp32's normal range only where the scale itself does
+    return m < 1.f ? m * k.rstd * k.pre / 127.f : m / 127.f * k.pre * k.rstd;
+}
+
+template <class T, int NE>
+__device__ __forceinline__ void add_frag(Frag<T, NE> &f, const Frag<T, NE> &g) {
+    float v[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] = f.at(i) + g.at(i);
+    f.set(v);
+}
+
+template <int MODE, class T, int NE>
+__device__ __forceinline__ void stats(const Frag<T, NE> &f, const float (&w)[NE], float &ss, float &m) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const float v = f.at(i);
+        if (norms(MODE)) ss = fmaf(v, v, ss);
+        if (MODE != kPlain) m = abs_max(m, weighs(MODE) ? v * w[i] : v);
+    }
+}
+
+// R rows per team of W lanes, NV fragments per lane and row.
+template <class T, int NE, int MODE, bool RES, int W, int NV, int R>
+__global__ void __launch_bounds__(kThreads) team_kernel(const FwdArgs a) {
+    const int64_t team = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / W;
+    const int t = threadIdx.x % W;
+    if ((((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) / W) * R >= a.N) return;   // a whole warp
+    const int64_t r0 = team * R;
+    Frag<T, NE> f[R][NV], g[R][NV];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+            f[i][j].zero();
+            if (r0 + i < a.N && col < a.d) {
+                f[i][j].load(static_cast<const T *>(a.x) + (r0 + i) * a.xs + col);
+                if (RES) g[i][j].load(static_cast<const T *>(a.res) + (r0 + i) * a.rs + col);
+            }
+        }
+    float w[NV][NE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int col = (j * W + t) * NE;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) w[j][i] = 1.f;
+        if (norms(MODE) && col < a.d) a.w.get<NE>(col, w[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float ss = 0.f;
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (RES && r0 + i < a.N && (j * W + t) * NE < a.d) add_frag(f[i][j], g[i][j]);
+            stats<MODE>(f[i][j], w[j], ss, m);
+        }
+        if (norms(MODE)) ss = team_reduce<W>(ss, Add());
+        if (MODE != kPlain) m = team_reduce<W>(m, AbsMax());
+        RowFactor k(ss, a.d, a.eps);
+        if (norms(MODE) && __any_sync(0xffffffffu, !(ss >= kLow && ss <= kHigh))) {
+            double t2 = 0;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) t2 += (double)f[i][j].at(e) * f[i][j].at(e);
+            t2 = team_reduce<W>(t2, Add());
+            if (!(ss >= kLow && ss <= kHigh)) k = RowFactor(t2, a.d, a.eps);   // not the warp's other rows
+            if (!isfinite(t2)) {
+                m = __int_as_float(0x7fc00000);
+                if (t == 0) flag(a.st, DBC_ERR_NONFINITE);
+            }
+        }
+        const Quant qn(m);
+        if (r0 + i < a.N) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (j * W + t) * NE;
+                if (col < a.d) write_frag<T, NE, MODE, RES>(a, r0 + i, col, f[i][j], w[j], k, qn);
+            }
+            if (MODE != kPlain && t == 0) {
+                a.scale[r0 + i] = row_scale<MODE>(qn, k);
+                if (qn.bad) flag(a.st, DBC_ERR_NONFINITE);
+            }
+        }
+    }
+}
+
+// One row per CTA of blockDim.x threads (a multiple of 32), NV fragments each.
+template <class T, int NE, int MODE, bool RES, int NV>
+__global__ void __launch_bounds__(1024) block_kernel(const FwdArgs a) {
+    __shared__ float s_ss[32];
+    __shared__ float s_m[32];
+    __shared__ double s_t[32];
+    const int t = threadIdx.x, W = blockDim.x, lane = t & 31, warp = t >> 5, warps = W >> 5;
     for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
-        const T *x = static_cast<const T *>(a.x) + r * a.xs;
-        const T *res = a.res ? static_cast<const T *>(a.res) + r * a.rs : nullptr;
-        T *s = a.s ? static_cast<T *>(a.s) + r * a.ss : nullptr;
-        auto val = [&](int i) { return res ? round_to<T>(ld_f(x + i) + ld_f(res + i)) : ld_f(x + i); };
-        float acc = 0.f, m = 0.f;
-        bool fin = true;
-        for (int i = threadIdx.x; i < a.d; i += kThreads) {
-            const float v = val(i);
-            acc = fmaf(v, v, acc);
-            fin &= isfinite(v);
-            if (MODE != kPlain) {
-                const float p = fabsf(MODE == kI8 ? v * a.w.at(i) : v);
-                fin &= isfinite(p);
-                m = fmaxf(m, p);
+        Frag<T, NE> f[NV], g[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+            f[j].zero();
+            if (col < a.d) {
+                f[j].load(static_cast<const T *>(a.x) + r * a.xs + col);
+                if (RES) g[j].load(static_cast<const T *>(a.res) + r * a.rs + col);
             }
         }
-        double ss = block_reduce(acc, add, sm);
-        fin = __syncthreads_and(fin) != 0;
-        if (!fin && threadIdx.x == 0) flag(a.st, DBC_ERR_NONFINITE);
-        if (MODE != kPlain) m = (float)block_reduce(m, mx, sm);
-        if (MODE != kQuantOnly && fin && !(ss >= 1e-30 && ss <= 1e37)) {
-            double t = 0;
-            for (int i = threadIdx.x; i < a.d; i += kThreads) {
-                const double v = val(i);
-                t += v * v;
-            }
-            ss = block_reduce(t, add, sm);
+        float w[NV][NE];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) w[j][i] = 1.f;
+            if (norms(MODE) && col < a.d) a.w.get<NE>(col, w[j]);
         }
-        const double rstd = 1.0 / sqrt(ss / a.d + (double)a.eps);
-        const Quant q(m, !fin);
-        for (int i = threadIdx.x; i < a.d; i += kThreads) {
-            const float v = val(i);
-            if (s) st_f(s + i, v);
-            if (MODE == kPlain) {
-                const float o = (float)(v * rstd * a.w.at(i));
-                if (a.y_bf16) st_f(static_cast<__nv_bfloat16 *>(a.y) + r * a.ys + i, o);
-                else st_f(static_cast<float *>(a.y) + r * a.ys + i, o);
-            } else {
-                a.q[r * a.qs + i] = (int8_t)q(MODE == kI8 ? v * a.w.at(i) : v);
-            }
+        float ss = 0.f;
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (RES && (j * W + t) * NE < a.d) add_frag(f[j], g[j]);
+            stats<MODE>(f[j], w[j], ss, m);
         }
-        if (MODE != kPlain && threadIdx.x == 0)
-            a.scale[r] = !fin ? __int_as_float(0x7fc00000) : MODE == kI8 ? (float)(m * rstd / 127.0) : m / 127.f;
+        if (norms(MODE)) ss = team_reduce<32>(ss, Add());
+        if (MODE != kPlain) m = team_reduce<32>(m, AbsMax());
+        if (lane == 0) {
+            s_ss[warp] = ss;
+            s_m[warp] = m;
+        }
         __syncthreads();
+        if (norms(MODE)) ss = team_reduce<32>(lane < warps ? s_ss[lane] : 0.f, Add());
+        if (MODE != kPlain) m = team_reduce<32>(lane < warps ? s_m[lane] : 0.f, AbsMax());
+        RowFactor k(ss, a.d, a.eps);
+        if (norms(MODE) && !(ss >= kLow && ss <= kHigh)) {     // the same in every thread
+            double t2 = 0;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) t2 += (double)f[j].at(e) * f[j].at(e);
+            t2 = team_reduce<32>(t2, Add());
+            if (lane == 0) s_t[warp] = t2;
+            __syncthreads();
+            t2 = team_reduce<32>(lane < warps ? s_t[lane] : 0.0, Add());
+            k = RowFactor(t2, a.d, a.eps);
+            if (!isfinite(t2)) {
+                m = __int_as_float(0x7fc00000);
+                if (t == 0) flag(a.st, DBC_ERR_NONFINITE);
+            }
+        }
+        const Quant qn(m);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+            if (col < a.d) write_frag<T, NE, MODE, RES>(a, r, col, f[j], w[j], k, qn);
+        }
+        if (MODE != kPlain && t == 0) {
+            a.scale[r] = row_scale<MODE>(qn, k);
+            if (qn.bad) flag(a.st, DBC_ERR_NONFINITE);
+        }
+        if (r + gridDim.x < a.N) __syncthreads();      // the shared words are written again
     }
 }
 
@@ -146,53 +245,248 @@ struct BwdArgs {
     int64_t ys, ss, ds_s, xs, N;
     int d;
     float eps;
-    float *part;
+    float *part;                 // one line of d dw sums per CTA, or NULL
     int32_t *st;
 };
 
-// One CTA walks rows r = blockIdx.x, + gridDim.x, ...; thread t owns columns
-// t, t + 256, ... and adds its rows' dw terms into its own line of `part`.
-template <class TY, class T>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(const BwdArgs a) {
-    __shared__ double sm[kThreads / 32];
-    auto add = [](double u, double v) { return u + v; };
-    float *part = a.part ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
-    if (part)
-        for (int i = threadIdx.x; i < a.d; i += kThreads) part[i] = 0.f;
-    for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
-        const TY *dy = static_cast<const TY *>(a.dy) + r * a.ys;
-        const T *s = static_cast<const T *>(a.s) + r * a.ss;
-        const T *ds = a.ds ? static_cast<const T *>(a.ds) + r * a.ds_s : nullptr;
-        T *dx = static_cast<T *>(a.dx) + r * a.xs;
-        double t2 = 0, tg = 0;
-        bool fin = true;
-        for (int i = threadIdx.x; i < a.d; i += kThreads) {
-            const double v = ld_f(s + i), g = (double)ld_f(dy + i) * a.w.at(i);
-            fin &= isfinite(v) && isfinite(g);
-            t2 += v * v;
-            tg += v * g;
+// One row's gradients, given its statistics: dx = rstd (g - xhat c) + ds with
+// c = mean(g xhat), and its terms dy * xhat added to acc.
+template <class TY, class T, int NE, bool DW>
+__device__ __forceinline__ void bwd_frag(const BwdArgs &a, int64_t r, int col, const Frag<TY, NE> &y,
+                                         const Frag<T, NE> &f, const float (&w)[NE], float rstd, float c,
+                                         float (&acc)[NE]) {
+    float o[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const float xh = f.at(i) * rstd;
+        o[i] = rstd * fmaf(-xh, c, y.at(i) * w[i]);
+        if (DW) acc[i] = fmaf(y.at(i), xh, acc[i]);
+    }
+    if (a.ds) {
+        Frag<T, NE> g;
+        g.load(static_cast<const T *>(a.ds) + r * a.ds_s + col);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) o[i] += g.at(i);
+    }
+    Frag<T, NE> q;
+    q.set(o);
+    q.store(static_cast<T *>(a.dx) + r * a.xs + col);
+}
+
+// The same in fp64, for rows whose sums leave fp32's range.
+template <class TY, class T, int NE, bool DW>
+__device__ __noinline__ void bwd_frag_wide(const BwdArgs &a, int64_t r, int col, const Frag<TY, NE> &y,
+                                           const Frag<T, NE> &f, const float (&w)[NE], double rstd, double c,
+                                           float (&acc)[NE]) {
+    Frag<T, NE> g;
+    g.zero();
+    if (a.ds) g.load(static_cast<const T *>(a.ds) + r * a.ds_s + col);
+    float o[NE];
+    for (int i = 0; i < NE; ++i) {
+        const double xh = f.at(i) * rstd, dy = y.at(i);
+        o[i] = (float)(rstd * (dy * w[i] - xh * c) + g.at(i));
+        if (DW) acc[i] += (float)(dy * xh);
+    }
+    g.set(o);
+    g.store(static_cast<T *>(a.dx) + r * a.xs + col);
+}
+
+template <class TY, class T, int NE>
+__device__ __forceinline__ void bwd_stats(const Frag<TY, NE> &y, const Frag<T, NE> &f, const float (&w)[NE],
+                                          float &ss, float &sg) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        ss = fmaf(f.at(i), f.at(i), ss);
+        sg = fmaf(y.at(i) * w[i], f.at(i), sg);
+    }
+}
+template <class TY, class T, int NE>
+__device__ __forceinline__ void bwd_stats_wide(const Frag<TY, NE> &y, const Frag<T, NE> &f, const float (&w)[NE],
+                                               double &ss, double &sg) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const double v = f.at(i);
+        ss += v * v;
+        sg += (double)y.at(i) * w[i] * v;
+    }
+}
+__device__ __forceinline__ bool in_range(float ss, float sg) { return ss >= kLow && ss <= kHigh && isfinite(sg); }
+
+// Teams of W lanes walk the rows R at a time; a lane keeps the dw sums of its
+// own columns in registers, the CTA joins them at the end (a fixed order).
+template <class TY, class T, int NE, bool DW, int W, int NV, int R>
+__global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
+    const int t = threadIdx.x % W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / W) * R;
+    float w[NV][NE], acc[NV][NE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int col = (j * W + t) * NE;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) w[j][i] = 1.f, acc[j][i] = 0.f;
+        if (col < a.d) a.w.get<NE>(col, w[j]);
+    }
+    // all teams of a warp take the same number of steps: the first team's rows decide
+    const int64_t first = ((int64_t)blockIdx.x * (kThreads / W) + (threadIdx.x & ~31) / W) * R;
+    for (int64_t rw = first; rw < a.N; rw += step) {
+        const int64_t r0 = rw + lane / W * R;
+        Frag<TY, NE> y[R][NV];
+        Frag<T, NE> f[R][NV];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (j * W + t) * NE;
+                y[i][j].zero();
+                f[i][j].zero();
+                if (r0 + i < a.N && col < a.d) {
+                    y[i][j].load(static_cast<const TY *>(a.dy) + (r0 + i) * a.ys + col);
+                    f[i][j].load(static_cast<const T *>(a.s) + (r0 + i) * a.ss + col);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float ss = 0.f, sg = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) bwd_stats(y[i][j], f[i][j], w[j], ss, sg);
+            ss = team_reduce<W>(ss, Add());
+            sg = team_reduce<W>(sg, Add());
+            const bool ok = in_range(ss, sg);
+            double s2 = 0, g2 = 0;
+            if (__any_sync(0xffffffffu, !ok)) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) bwd_stats_wide(y[i][j], f[i][j], w[j], s2, g2);
+                s2 = team_reduce<W>(s2, Add());
+                g2 = team_reduce<W>(g2, Add());
+                if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
+            }
+            const float rstd = rsqrtf(ss / (float)a.d + a.eps), c = sg / (float)a.d * rstd;
+            const double rstd2 = ok ? 0 : 1.0 / sqrt(s2 / a.d + (double)a.eps), c2 = ok ? 0 : g2 / a.d * rstd2;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (j * W + t) * NE;
+                if (r0 + i < a.N && col < a.d) {
+                    if (ok) bwd_frag<TY, T, NE, DW>(a, r0 + i, col, y[i][j], f[i][j], w[j], rstd, c, acc[j]);
+                    else bwd_frag_wide<TY, T, NE, DW>(a, r0 + i, col, y[i][j], f[i][j], w[j], rstd2, c2, acc[j]);
+                }
+            }
         }
-        t2 = block_reduce(t2, add, sm);
-        tg = block_reduce(tg, add, sm);
-        if (!__syncthreads_and(fin) && threadIdx.x == 0) flag(a.st, DBC_ERR_NONFINITE);
-        const double rstd = 1.0 / sqrt(t2 / a.d + (double)a.eps);
-        const double c = tg / a.d * rstd * rstd;
-        for (int i = threadIdx.x; i < a.d; i += kThreads) {
-            const double v = ld_f(s + i), y = ld_f(dy + i);
-            double o = rstd * (y * a.w.at(i) - v * c);
-            if (ds) o += ld_f(ds + i);
-            st_f(dx + i, (float)o);
-            if (part) part[i] += (float)(y * v * rstd);
+    }
+    if constexpr (DW) {
+        __shared__ float sm[kThreads / 32][NV * W * NE];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                float v = acc[j][i];
+#pragma unroll
+                for (int o = W; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane < W) sm[warp][(j * W + t) * NE + i] = v;
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.d; c += kThreads) {
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < kThreads / 32; ++k) v += sm[k][c];
+            a.part[(int64_t)blockIdx.x * a.d + c] = v;
         }
     }
 }
 
-__global__ void __launch_bounds__(kThreads) dw_kernel(const float *part, int rows, int d, float *dw) {
-    const int i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= d) return;
+// Wide rows: one row per CTA at a time, NV fragments per thread.
+template <class TY, class T, int NE, bool DW, int NV>
+__global__ void __launch_bounds__(1024) bwd_block_kernel(const BwdArgs a) {
+    __shared__ float2 part[2][32];
+    __shared__ double2 wide[32];
+    const int t = threadIdx.x, W = blockDim.x, lane = t & 31, warp = t >> 5, warps = W >> 5;
+    float acc[NV][NE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < NE; ++i) acc[j][i] = 0.f;
+    int ph = 0;
+    for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, ph ^= 1) {
+        Frag<TY, NE> y[NV];
+        Frag<T, NE> f[NV];
+        float w[NV][NE];
+        float ss = 0.f, sg = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+            y[j].zero();
+            f[j].zero();
+            if (col < a.d) {
+                y[j].load(static_cast<const TY *>(a.dy) + r * a.ys + col);
+                f[j].load(static_cast<const T *>(a.s) + r * a.ss + col);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) w[j][i] = 1.f;
+            if (col < a.d) a.w.get<NE>(col, w[j]);
+            bwd_stats(y[j], f[j], w[j], ss, sg);
+        }
+        ss = team_reduce<32>(ss, Add());
+        sg = team_reduce<32>(sg, Add());
+        if (lane == 0) part[ph][warp] = make_float2(ss, sg);
+        __syncthreads();             // the other buffer's readers are past the previous row's barrier
+        const float2 v = lane < warps ? part[ph][lane] : make_float2(0.f, 0.f);
+        ss = team_reduce<32>(v.x, Add());
+        sg = team_reduce<32>(v.y, Add());
+        if (in_range(ss, sg)) {      // the same in every thread
+            const float rstd = rsqrtf(ss / (float)a.d + a.eps), c = sg / (float)a.d * rstd;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (j * W + t) * NE;
+                if (col < a.d) bwd_frag<TY, T, NE, DW>(a, r, col, y[j], f[j], w[j], rstd, c, acc[j]);
+            }
+        } else {
+            double s2 = 0, g2 = 0;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
+            s2 = team_reduce<32>(s2, Add());
+            g2 = team_reduce<32>(g2, Add());
+            if (lane == 0) wide[warp] = make_double2(s2, g2);
+            __syncthreads();
+            const double2 v2 = lane < warps ? wide[lane] : make_double2(0, 0);
+            s2 = team_reduce<32>(v2.x, Add());
+            g2 = team_reduce<32>(v2.y, Add());
+            if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
+            const double rstd = 1.0 / sqrt(s2 / a.d + (double)a.eps), c = g2 / a.d * rstd;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (j * W + t) * NE;
+                if (col < a.d) bwd_frag_wide<TY, T, NE, DW>(a, r, col, y[j], f[j], w[j], rstd, c, acc[j]);
+            }
+        }
+    }
+    if constexpr (DW) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int col = (j * W + t) * NE + i;
+                if (col < a.d) a.part[(int64_t)blockIdx.x * a.d + col] = acc[j][i];
+            }
+    }
+}
+
+// dw = the CTAs' lines added up, in a fixed order: 32 columns per CTA, 32
+// threads per column.
+__global__ void __launch_bounds__(1024) dw_kernel(const float *part, int lines, int d, float *dw) {
+    __shared__ double sm[32][33];
+    const int c = threadIdx.x & 31, k = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
     double t = 0;
-    for (int r = 0; r < rows; ++r) t += part[(int64_t)r * d + i];
-    dw[i] = (float)t;
+    if (col < d) {
+#pragma unroll 8
+        for (int r = k; r < lines; r += 32) t += part[(int64_t)r * d + col];
+    }
+    sm[k][c] = t;
+    __syncthreads();
+    t = team_reduce<32>(sm[c][k], Add());
+    if (c == 0 && blockIdx.x * 32 + k < d) dw[blockIdx.x * 32 + k] = (float)t;
 }
 
 inline bool aligned_to(const void *p, int64_t e) { return (reinterpret_cast<uintptr_t>(p) % e) == 0; }
@@ -214,16 +508,119 @@ inline dbc_status check_fwd(const FwdArgs &a, int dtype, int w_dtype, int64_t d,
     return DBC_OK;
 }
 
+// Whether rows of `stride` elements of `esz` bytes at p all start on multiples
+// of `unit` bytes.
+inline bool on_grid(const void *p, int64_t stride, int64_t esz, int64_t unit) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % unit == 0 && stride * esz % unit == 0);
+}
+
+template <class T, int NE, int MODE, int W, int NV, int R>
+dbc_status launch_team(const FwdArgs &a, cudaStream_t st) {
+    const int64_t teams = (a.N + R - 1) / R, grid = (teams * W + kThreads - 1) / kThreads;
+    if (grid > INT32_MAX) return DBC_ERR_UNSUPPORTED;
+    if constexpr (norms(MODE)) {
+        if (a.res) {
+            team_kernel<T, NE, MODE, true, W, NV, R><<<(unsigned)grid, kThreads, 0, st>>>(a);
+            return DBC_OK;
+        }
+    }
+    team_kernel<T, NE, MODE, false, W, NV, R><<<(unsigned)grid, kThreads, 0, st>>>(a);
+    return DBC_OK;
+}
+
+template <class T, int NE, int MODE, int NV>
+dbc_status launch_block(const FwdArgs &a, cudaStream_t st) {
+    const int threads = ((a.d + NE * NV - 1) / (NE * NV) + 31) / 32 * 32;
+    const unsigned grid = (unsigned)std::min<int64_t>(a.N, INT32_MAX);
+    if constexpr (norms(MODE)) {
+        if (a.res) {
+            block_kernel<T, NE, MODE, true, NV><<<grid, threads, 0, st>>>(a);
+            return DBC_OK;
+        }
+    }
+    block_kernel<T, NE, MODE, false, NV><<<grid, threads, 0, st>>>(a);
+    return DBC_OK;
+}
+
+// Several rows per team pay once every SM has work without them.
+inline bool many(int64_t rows, int lanes, int R) { return rows * lanes / 32 / R >= 148 * 16; }
+
+template <class T, int MODE>
+dbc_status launch_rows(const FwdArgs &a, cudaStream_t st) {
+    constexpr int E = 16 / sizeof(T);
+    const int64_t e = sizeof(T), ysz = a.y_bf16 ? 2 : 4;
+    const bool vec = a.d % E == 0 && on_grid(a.x, a.xs, e, 16) && on_grid(a.res, a.rs, e, 16) &&
+                     on_grid(a.s, a.ss, e, 16) && on_grid(a.y, a.ys, ysz, std::min<int64_t>(16, E * ysz)) &&
+                     on_grid(a.q, a.qs, 1, E) && on_grid(a.w.p, 0, 1, a.w.bf16 ? E * 2 : 16);
+    if (!vec) {
+        if (a.d <= 256) return launch_team<T, 1, MODE, 32, 8, 1>(a, st);
+        if (a.d <= 512) return launch_team<T, 1, MODE, 32, 16, 1>(a, st);
+        return launch_block<T, 1, MODE, 16>(a, st);
+    }
+    const int V = a.d / E;
+    if (V <= 8)
+        return many(a.N, 8, 4) ? launch_team<T, E, MODE, 8, 1, 4>(a, st) : launch_team<T, E, MODE, 8, 1, 1>(a, st);
+    if (V <= 16)
+        return many(a.N, 16, 4) ? launch_team<T, E, MODE, 16, 1, 4>(a, st) : launch_team<T, E, MODE, 16, 1, 1>(a, st);
+    if (V <= 32)
+        return many(a.N, 32, 4) ? launch_team<T, E, MODE, 32, 1, 4>(a, st) : launch_team<T, E, MODE, 32, 1, 1>(a, st);
+    if (V <= 64)
+        return many(a.N, 32, 2) ? launch_team<T, E, MODE, 32, 2, 2>(a, st) : launch_team<T, E, MODE, 32, 2, 1>(a, st);
+    if (V <= 128) return launch_team<T, E, MODE, 32, 4, 1>(a, st);
+    if (V <= 2048) return launch_block<T, E, MODE, 2>(a, st);
+    return launch_block<T, E, MODE, 4>(a, st);
+}
+
 template <int MODE>
 dbc_status launch_fwd(const FwdArgs &a, int dtype, cudaStream_t st) {
-    const int grid = (int)std::min<int64_t>(a.N, (int64_t)num_sms() * 8);
-    if (dtype == DBC_BF16) norm_kernel<__nv_bfloat16, MODE><<<grid, kThreads, 0, st>>>(a);
-    else norm_kernel<float, MODE><<<grid, kThreads, 0, st>>>(a);
+    // bf16 rows under a bf16 weight (or none) give products of 16 significant bits
+    constexpr int kBf16Mode = MODE == kI8 ? kI8Narrow : MODE;
+    const dbc_status c = dtype != DBC_BF16              ? launch_rows<float, MODE>(a, st)
+                         : !a.w.p || a.w.bf16 ? launch_rows<__nv_bfloat16, kBf16Mode>(a, st)
+                                              : launch_rows<__nv_bfloat16, MODE>(a, st);
+    if (c != DBC_OK) return c;
     count_launches(1);
     return launch_status();
 }
 
-inline int bwd_grid(int64_t N) { return (int)std::min<int64_t>(std::max<int64_t>(N, 1), 148 * 4); }
+// CTAs of a backward call, and with them the lines of dw sums: up to 8 per SM,
+// fewer for wide rows, whose lines would otherwise outweigh the rows.
+inline int bwd_ctas(int64_t N, int64_t d) {
+    return (int)std::min<int64_t>(N, 148 * std::min<int64_t>(8, std::max<int64_t>(1, kMaxD / d)));
+}
+
+template <class TY, class T, int NE, int W, int NV, int R>
+void launch_bwd_team(const BwdArgs &a, int ctas, cudaStream_t st) {
+    if (a.part) bwd_team_kernel<TY, T, NE, true, W, NV, R><<<ctas, kThreads, 0, st>>>(a);
+    else bwd_team_kernel<TY, T, NE, false, W, NV, R><<<ctas, kThreads, 0, st>>>(a);
+}
+
+template <class TY, class T, int NE, int NV>
+void launch_bwd_block(const BwdArgs &a, int ctas, cudaStream_t st) {
+    const int threads = ((a.d + NE * NV - 1) / (NE * NV) + 31) / 32 * 32;
+    if (a.part) bwd_block_kernel<TY, T, NE, true, NV><<<ctas, threads, 0, st>>>(a);
+    else bwd_block_kernel<TY, T, NE, false, NV><<<ctas, threads, 0, st>>>(a);
+}
+
+template <class TY, class T>
+void launch_bwd(const BwdArgs &a, int ctas, cudaStream_t st) {
+    constexpr int E = 16 / sizeof(T);
+    const int64_t e = sizeof(T), ey = sizeof(TY);
+    const bool vec = a.d % E == 0 && on_grid(a.s, a.ss, e, 16) && on_grid(a.ds, a.ds_s, e, 16) &&
+                     on_grid(a.dx, a.xs, e, 16) && on_grid(a.dy, a.ys, ey, std::min<int64_t>(16, E * ey)) &&
+                     on_grid(a.w.p, 0, 1, a.w.bf16 ? E * 2 : 16);
+    if (!vec) {
+        if (a.d <= 256) return launch_bwd_team<TY, T, 1, 32, 8, 1>(a, ctas, st);
+        return launch_bwd_block<TY, T, 1, 16>(a, ctas, st);
+    }
+    const int V = a.d / E;
+    if (V <= 8) return launch_bwd_team<TY, T, E, 8, 1, 2>(a, ctas, st);
+    if (V <= 16) return launch_bwd_team<TY, T, E, 16, 1, 2>(a, ctas, st);
+    if (V <= 32) return launch_bwd_team<TY, T, E, 32, 1, 2>(a, ctas, st);
+    if (V <= 64) return launch_bwd_team<TY, T, E, 32, 2, 1>(a, ctas, st);
+    if (V <= 2048) return launch_bwd_block<TY, T, E, 2>(a, ctas, st);
+    return launch_bwd_block<TY, T, E, 4>(a, ctas, st);
+}
 
 }  // namespace nm
 }  // namespace dbc
@@ -271,12 +668,12 @@ extern "C" dbc_status quantize_rows_i8(const void *x, int64_t x_stride, int dtyp
     if (q_stride < d) return DBC_ERR_INVALID_ARG;
     if (N == 0) return DBC_OK;
     if (!q || !scale || !nm::aligned_to(scale, 4)) return DBC_ERR_INVALID_ARG;
-    return nm::launch_fwd<nm::kQuantOnly>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
+    return nm::launch_fwd<nm::kQuant>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t rms_norm_backward_workspace(int64_t N, int64_t d) {
     if (N <= 0 || d <= 0) return 0;
-    return align_up((size_t)nm::bwd_grid(N) * (size_t)d * sizeof(float));
+    return align_up((size_t)nm::bwd_ctas(N, d) * (size_t)d * sizeof(float));
 }
 
 extern "C" dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int dy_dtype, const void *s,
@@ -301,17 +698,15 @@ extern "C" dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int d
     }
     if (dw && (!ws || !nm::aligned_to(ws, 16) || ws_bytes < rms_norm_backward_workspace(N, d)))
         return DBC_ERR_WORKSPACE;
-    const int grid = nm::bwd_grid(N);
-    nm::BwdArgs a{dy, s, ds, dx, {weight, w_dtype == DBC_BF16}, dy_stride, s_stride, ds_stride, dx_stride, N, (int)d,
-                  eps, dw ? static_cast<float *>(ws) : nullptr, dev_status};
+    const int ctas = nm::bwd_ctas(N, d);
+    const nm::BwdArgs a{dy, s, ds, dx, {weight, w_dtype == DBC_BF16}, dy_stride, s_stride, ds_stride, dx_stride, N,
+                        (int)d, eps, dw ? static_cast<float *>(ws) : nullptr, dev_status};
     using B = __nv_bfloat16;
-    if (dy_dtype == DBC_BF16 && dtype == DBC_BF16) nm::bwd_kernel<B, B><<<grid, nm::kThreads, 0, st>>>(a);
-    else if (dy_dtype == DBC_BF16) nm::bwd_kernel<B, float><<<grid, nm::kThreads, 0, st>>>(a);
-    else if (dtype == DBC_BF16) nm::bwd_kernel<float, B><<<grid, nm::kThreads, 0, st>>>(a);
-    else nm::bwd_kernel<float, float><<<grid, nm::kThreads, 0, st>>>(a);
+    if (dy_dtype == DBC_BF16 && dtype == DBC_BF16) nm::launch_bwd<B, B>(a, ctas, st);
+    else if (dy_dtype == DBC_BF16) nm::launch_bwd<B, float>(a, ctas, st);
+    else if (dtype == DBC_BF16) nm::launch_bwd<float, B>(a, ctas, st);
+    else nm::launch_bwd<float, float>(a, ctas, st);
+    if (dw) nm::dw_kernel<<<(unsigned)((d + 31) / 32), 1024, 0, st>>>(static_cast<const float *>(ws), ctas, (int)d, dw);
     count_launches(dw ? 2 : 1);
-    if (dw)
-        nm::dw_kernel<<<(unsigned)((d + nm::kThreads - 1) / nm::kThreads), nm::kThreads, 0, st>>>(
-            static_cast<const float *>(ws), grid, (int)d, dw);
     return launch_status();
 }

@@ -1,0 +1,297 @@
+// Building blocks of the norm kernels: row fragments in registers, team
+// reductions, the 8-bit code.
+#pragma once
+
+#include "common.cuh"
+
+namespace dbc {
+namespace nm {
+
+// NE consecutive elements of a row in registers: 16 bytes (NE = 8 bf16 or 4
+// fp32), or one element (NE = 1, rows off the 16-byte grid and odd widths).
+// Rows bypass L1 (read once); what all rows share is kept there.
+template <class T, int NE>
+struct Frag;
+
+template <>
+struct Frag<__nv_bfloat16, 8> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(p));
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    }
+    __device__ __forceinline__ void load_shared_by_rows(const __nv_bfloat16 *p) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+    __device__ __forceinline__ float at(int i) const {
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+};
+
+template <>
+struct Frag<__nv_bfloat16, 4> {
+    uint32_t w[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(p));
+        w[0] = u.x, w[1] = u.y;
+    }
+    __device__ __forceinline__ void load_shared_by_rows(const __nv_bfloat16 *p) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+        w[0] = u.x, w[1] = u.y;
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = 0; }
+    __device__ __forceinline__ float at(int i) const {
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    __device__ __forceinline__ void set(const float (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+};
+
+template <>
+struct Frag<__nv_bfloat16, 1> {
+    __nv_bfloat16 b;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        const uint16_t u = __ldcg(reinterpret_cast<const unsigned short *>(p));
+        b = __ushort_as_bfloat16(u);
+    }
+    __device__ __forceinline__ void load_shared_by_rows(const __nv_bfloat16 *p) {
+        b = __ushort_as_bfloat16(__ldg(reinterpret_cast<const unsigned short *>(p)));
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *p = b; }
+    __device__ __forceinline__ void zero() { b = __ushort_as_bfloat16(0); }
+    __device__ __forceinline__ float at(int) const { return __bfloat162float(b); }
+    __device__ __forceinline__ void set(const float (&v)[1]) { b = __float2bfloat16_rn(v[0]); }
+};
+
+template <int NE>
+struct Frag<float, NE> {
+    static_assert(NE == 8 || NE == 4 || NE == 1, "");
+    float v[NE];
+    __device__ __forceinline__ void load(const float *p) {
+        if constexpr (NE == 1) {
+            v[0] = __ldcg(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE / 4; ++i) {
+                const float4 u = __ldcg(reinterpret_cast<const float4 *>(p) + i);
+                v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void load_shared_by_rows(const float *p) {
+        if constexpr (NE == 1) {
+            v[0] = __ldg(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE / 4; ++i) {
+                const float4 u = __ldg(reinterpret_cast<const float4 *>(p) + i);
+                v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float *p) const {
+        if constexpr (NE == 1) {
+            *p = v[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE / 4; ++i)
+                reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] = 0.f;
+    }
+    __device__ __forceinline__ float at(int i) const { return v[i]; }
+    __device__ __forceinline__ void set(const float (&u)[NE]) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] = u[i];
+    }
+};
+
+// The weight: fp32 or bf16, NULL reads as ones.
+struct Weight {
+    const void *p;
+    int bf16;
+    template <int NE>
+    __device__ __forceinline__ void get(int64_t i, float (&out)[NE]) const {
+        if (!p) {
+#pragma unroll
+            for (int k = 0; k < NE; ++k) out[k] = 1.f;
+        } else if (bf16) {
+            Frag<__nv_bfloat16, NE> f;
+            f.load_shared_by_rows(static_cast<const __nv_bfloat16 *>(p) + i);
+#pragma unroll
+            for (int k = 0; k < NE; ++k) out[k] = f.at(k);
+        } else {
+            Frag<float, NE> f;
+            f.load_shared_by_rows(static_cast<const float *>(p) + i);
+#pragma unroll
+            for (int k = 0; k < NE; ++k) out[k] = f.at(k);
+        }
+    }
+};
+
+template <int NE>
+__device__ __forceinline__ void store_as(void *base, int bf16, int64_t i, const float (&v)[NE]) {
+    if (bf16) {
+        Frag<__nv_bfloat16, NE> f;
+        f.set(v);
+        f.store(static_cast<__nv_bfloat16 *>(base) + i);
+    } else {
+        Frag<float, NE> f;
+        f.set(v);
+        f.store(static_cast<float *>(base) + i);
+    }
+}
+
+// Packed pairs of fp32 (one instruction per pair on sm_100).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
+        " mov.b64 {%0, %1}, z;\n}\n" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n"
+        " mov.b64 {%0, %1}, z;\n}\n" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n" : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// max(m, |v|), NaN if either is.
+__device__ __forceinline__ float abs_max(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+
+// How a row is quantised, from its m = max |p|.
+//
+// The code is rint(127 p / m), halves to even, and it has to be the exact
+// quotient's: with bf16 inputs one quotient in a few hundred IS a half.  The
+// quotient t of a = 127 p comes from the reciprocal and one residual step, so
+// it is a / m rounded once (but for 2^-23 of a step); adding 1.5 * 2^23 rounds t to a whole number
+// (halves to even) and leaves it in the low bits.
+//   NARROW (p has 16 significant bits: a bf16 value, or a product of two): a is
+//   exact, and a / m is a half-integer h or at least h 2^-23.99 away from it
+//   (254 P 2^e - (2k + 1) M is a multiple of 2^e, and 2^e >= h M / (127 * 2^16)),
+//   more than the h 2^-24 that t is rounded by: t decides.
+//   Otherwise t is off by up to 1.6e-5, and quotients closer than that to a half
+//   (one fp32 value in ten thousand) are settled by the sign of 127 p - h m, with
+//   127 p in two exact pieces; the difference from h m cancels to a few bits, so
+//   it is exact too.
+struct Quant {
+    float m, rinv;
+    bool bad;
+    __device__ __forceinline__ explicit Quant(float m_) {
+        bad = !(m_ <= 3.4028234e38f);
+        m = bad ? 0.f : m_;
+        rinv = m > 0.f ? 1.f / m : 0.f;
+    }
+    template <bool NARROW>
+    __device__ __forceinline__ static float settle(float p, float m, float v, float t) {
+        constexpr float kMagic = 12582912.f;
+        const float r = v - kMagic, e = t - r;
+        if (NARROW || fabsf(e) < 0.5f - 4e-5f) return v;
+        const float h = r + copysignf(0.5f, e);
+        const float hi = 127.f * p, lo = fmaf(127.f, p, -hi);
+        const float d = fmaf(-h, m, hi) + lo;
+        // just above or below h, or on it: the even neighbour (h + 1.5 * 2^23 would round to it too)
+        const float f = d > 0.f ? h + 0.5f : d < 0.f ? h - 0.5f : rintf(h);
+        return f + kMagic;
+    }
+    template <bool NARROW, int NE>
+    __device__ __forceinline__ void store(int8_t *q, const float (&p_)[NE]) const {
+        constexpr float kMagic = 12582912.f;
+        uint32_t u[NE];
+        float p[NE], ms = m, rs = rinv;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) p[i] = p_[i];
+        if (ms < 0x1p-60f || ms > 0x1p100f) {          // reciprocal or residual could leave fp32's range
+            const float k = ms < 1.f ? 0x1p80f : 0x1p-80f;
+            ms *= k;
+            rs = ms > 0.f ? 1.f / ms : 0.f;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) p[i] *= k;    // exact, or too small to matter
+        }
+        if constexpr (NE == 1) {
+            const float a = 127.f * p[0], t0 = a * rs, t = fmaf(fmaf(-t0, ms, a), rs, t0);
+            u[0] = __float_as_uint(settle<NARROW>(p[0], ms, t + kMagic, t));
+        } else {
+            const float2 c127 = make_float2(127.f, 127.f), mm = make_float2(-ms, -ms), rr = make_float2(rs, rs);
+#pragma unroll
+            for (int i = 0; i < NE; i += 2) {
+                const float2 a = mul2(make_float2(p[i], p[i + 1]), c127);
+                const float2 t0 = mul2(a, rr);
+                const float2 t = fma2(fma2(t0, mm, a), rr, t0);
+                const float2 v = add2(t, make_float2(kMagic, kMagic));
+                u[i] = __float_as_uint(settle<NARROW>(p[i], ms, v.x, t.x));
+                u[i + 1] = __float_as_uint(settle<NARROW>(p[i + 1], ms, v.y, t.y));
+            }
+        }
+        if (bad) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) u[i] = 0;
+        }
+        if constexpr (NE == 1) {
+            *q = (int8_t)u[0];
+        } else {
+            uint32_t w[NE / 4];
+#pragma unroll
+            for (int i = 0; i < NE / 4; ++i)
+                w[i] = __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040),
+                                   __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040), 0x5410);
+            if constexpr (NE == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t *>(q) = w[0];
+        }
+    }
+};
+
+struct Add {
+    template <class V>
+    __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
+};
+struct AbsMax {
+    __device__ __forceinline__ float operator()(float a, float b) const { return abs_max(a, b); }
+};
+
+// Reduction over teams of W consecutive lanes (a power of two up to 32); all
+// 32 lanes take part, every lane gets its team's result.
+template <int W, class V, class F>
+__device__ __forceinline__ V team_reduce(V v, F f) {
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+}  // namespace nm
+}  // namespace dbc
