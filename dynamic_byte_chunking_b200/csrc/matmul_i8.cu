@@ -1,6 +1,25 @@
 // matmul_i8: out = a_scale * b_scale * (a b^T) (+ bias), int8 operands with
 // exact int32 sums (formula and arguments at the declaration in dbc.h).
-#include "common.cuh"
+//
+// Both kernels feed kind::i8 tcgen05 MMAs (128 x N x 32 per instruction, sums
+// in TMEM) from a ring of TMA-loaded, 128-byte swizzled stages of 128 bytes of
+// K; TMA's zero fill pads odd depths and row counts.
+//   * wide_kernel: 128 tokens x 128 channels per tile, one persistent CTA per
+//     SM; loads, MMAs and the epilogue of the previous tile (two accumulators)
+//     run at the same time.  Outputs leave through swizzled staging and TMA tile
+//     stores.
+//   * split_kernel: for few tokens or few tiles.  128 CHANNELS sit on the TMEM
+//     lanes and the tokens on its columns, so that one token costs 16 columns
+//     and not 128 lanes; the depth is split over a cluster of up to 8 CTAs,
+//     whose partial sums (integers: any order gives the same) are joined through
+//     distributed shared memory.
+// Every wait is bounded; a timeout flags DBC_ERR_TIMEOUT and the CTA skips its
+// remaining work, after waiting for its copies and MMAs in flight.
+#include <cuda.h>
+#include <string.h>
+
+#include "tc.cuh"
+#include "tma_host.cuh"
 
 namespace dbc {
 namespace mi {
@@ -9,12 +28,11 @@ constexpr int64_t kMaxK = 131071;                // K * 128 * 128 < 2^31
 constexpr int64_t kMaxMN = (1ll << 31) - 1024;   // tile origins stay in 32 bits
 
 struct Args {
-    const int8_t *a, *b;
     const float *as, *bs;
     const void *bias;
     void *out;
-    int64_t lda, ldb, ldo, M, N;
-    int K, bias_bf16, out_bf16;
+    int64_t ldo;
+    int M, N, K, bias_bf16, out_bf16;
     int32_t *st;
 };
 
@@ -24,50 +42,403 @@ __device__ __forceinline__ float bias_at(const Args &p, int64_t j) {
                        : static_cast<const float *>(p.bias)[j];
 }
 
-// 64 x 64 outputs per CTA of 256 threads, 4 x 4 each, with the packed 4-byte
-// dot product; K in steps of 64 bytes through shared memory.
-__global__ void __launch_bounds__(256) dot_kernel(const Args p) {
-    __shared__ int A[64][17], B[64][17];
-    const int64_t m0 = (int64_t)blockIdx.x * 64;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t n0 = (int64_t)blockIdx.y * 64; n0 < p.N; n0 += (int64_t)gridDim.y * 64) {
-        int acc[4][4] = {};
-        for (int k0 = 0; k0 < p.K; k0 += 64) {
-            const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 16;
-            auto fetch = [&](const int8_t *base, int64_t ld, int64_t row, int64_t rows, int *dst) {
-                int4 v = make_int4(0, 0, 0, 0);
-                // rows start on 16 bytes and ld >= K is a multiple of 16, so the piece that holds
-                // byte k0 + c < K lies inside the row
-                if (row < rows && k0 + c < p.K) v = *reinterpret_cast<const int4 *>(base + row * ld + k0 + c);
-                int w[4] = {v.x, v.y, v.z, v.w};
+// The four (at the end of the depth: fewer) K steps of one stage.
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sa, uint32_t sb, uint32_t idesc, int left, bool first) {
+    const uint64_t da = tc::sdesc(sa, 16, 1024), db = tc::sdesc(sb, 16, 1024);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int left = p.K - (k0 + c + 4 * i);   // bytes of this word inside the row
-                    dst[i] = left >= 4 ? w[i] : left <= 0 ? 0 : w[i] & ((1 << (8 * left)) - 1);
-                }
-            };
-            fetch(p.a, p.lda, m0 + r, p.M, &A[r][c / 4]);
-            fetch(p.b, p.ldb, n0 + r, p.N, &B[r][c / 4]);
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(A[ty + 16 * i][k], B[tx + 16 * j][k], acc[i][j]);
-            __syncthreads();
+    for (int k = 0; k < 4; ++k)
+        if (k * 32 < left)
+            tc::mma_i8(d, tc::sdesc_add(da, k * 32), tc::sdesc_add(db, k * 32), idesc, first && k == 0 ? 0u : 1u);
+}
+
+// ---------------------------------------------------------------- many tiles
+struct Wide {
+    static constexpr int BM = 128, BN = 128, NS = 5, EPI = 8;             // EPI epilogue warps
+    static constexpr int THREADS = 64 + EPI * 32;
+    static constexpr uint32_t A = BM * 128, B = BN * 128, STAGE = A + B;
+    static constexpr uint32_t SLAB = 32 * 128;                            // one warp's rows x 128 bytes
+    static constexpr size_t SMEM = NS * STAGE + EPI * SLAB + 1024;
+};
+
+struct Tile {
+    int m, n;
+};
+// Tiles in groups of 16 column blocks, rows outermost inside a group: the CTAs
+// that run together share their rows of a and a group's rows of b in L2.
+__device__ __forceinline__ Tile tile_at(int64_t i, int mt, int nt) {
+    const int64_t full = (int64_t)mt * 16;
+    const int g = (int)(i / full);
+    const int64_t rem = i - g * full;
+    const int w = min(16, nt - g * 16);
+    return {(int)(rem / w), g * 16 + (int)(rem % w)};
+}
+
+template <bool TMA_OUT>
+__global__ void __launch_bounds__(Wide::THREADS, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                const __grid_constant__ CUtensorMap to, const Args p) {
+    using C = Wide;
+    extern __shared__ uint8_t smraw[];
+    __shared__ uint64_t full[C::NS], empty[C::NS], tfull[2], tempty[2], drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ __align__(16) float2 sc[2][C::BN];      // per channel: scale, bias
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (tc::smem_u32(smraw) + 1023u) & ~1023u;
+    uint8_t *const sgen = smraw + (base - tc::smem_u32(smraw));
+    if (warp == 1) tc::tmem_alloc(&tmem_base, 2 * C::BN);
+    if (tid == 0) {
+        for (int i = 0; i < C::NS; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + ty + 16 * i;
-            for (int j = 0; j < 4; ++j) {
-                const int64_t n = n0 + tx + 16 * j;
-                if (m >= p.M || n >= p.N) continue;
-                const float v = (float)acc[i][j] * p.as[m] * p.bs[n] + bias_at(p, n);
-                if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
-                else static_cast<float *>(p.out)[m * p.ldo + n] = v;
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&tfull[i], 1);
+            tc::mbar_init(&tempty[i], C::EPI);
+        }
+        tc::mbar_init(&drain, 1);
+        tc::fence_mbar_init();
+        tc::tma_prefetch_desc(&ta);
+        tc::tma_prefetch_desc(&tb);
+        if (TMA_OUT) tc::tma_prefetch_desc(&to);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tbase = tmem_base;
+    const int mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN, ks = (p.K + 127) / 128;
+    const int64_t tiles = (int64_t)mt * nt;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0, issued = 0;                       // stage; copies since the start, up to NS
+            uint32_t ph = 1;                             // parity of the stage's last release
+            bool ok = true;
+            for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+                const Tile t = tile_at(i, mt, nt);
+                for (int k = 0; k < ks; ++k) {
+                    if (issued == C::NS && !(ok = tc::mbar_wait(&empty[s], ph, p.st))) break;
+                    issued += issued < C::NS;
+                    const uint32_t sa = base + s * C::STAGE;
+                    tc::mbar_arrive_expect_tx(&full[s], C::STAGE);
+                    tc::tma_load_2d(sa, &ta, &full[s], k * 128, t.m * C::BM);
+                    tc::tma_load_2d(sa + C::A, &tb, &full[s], k * 128, t.n * C::BN);
+                    if (++s == C::NS) s = 0, ph ^= 1;
+                }
+            }
+            // after a timeout: every stage's last copies land before the CTA ends
+            if (!ok)
+                for (int k = 0; k < C::NS; ++k) tc::mbar_wait(&full[k], k < s ? ph ^ 1 : ph, p.st);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = tc::idesc_i8(C::BM, C::BN);
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t n = 0;
+            bool ok = true;
+            for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x, ++n) {
+                const int b = (int)(n & 1);
+                if (n >= 2 && !(ok = tc::mbar_wait(&tempty[b], (uint32_t)(n / 2 - 1) & 1u, p.st))) break;
+                tc::fence_after_sync();
+                for (int k = 0; k < ks; ++k) {
+                    if (!(ok = tc::mbar_wait(&full[s], ph, p.st))) break;
+                    tc::fence_after_sync();
+                    const uint32_t sa = base + s * C::STAGE;
+                    mma_stage(tbase + b * C::BN, sa, sa + C::A, idesc, p.K - k * 128, k == 0);
+                    tc::mma_commit(&empty[s]);
+                    if (++s == C::NS) s = 0, ph ^= 1;
+                }
+                if (ok) tc::mma_commit(&tfull[b]);
+            }
+            if (!ok) {
+                tc::mma_commit(&drain);
+                tc::mbar_wait(&drain, 0, p.st);
             }
         }
+    } else {
+        // warp w reads TMEM lanes (w % 4) * 32 .. + 31 and one half of the columns
+        const int q = warp & 3, half = (warp - 2) >> 2, et = tid - 64;
+        uint8_t *const slab = sgen + C::NS * C::STAGE + (warp - 2) * C::SLAB;
+        const int cols = p.out_bf16 ? 64 : 32;           // columns of a slab
+        int64_t n = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x, ++n) {
+            const Tile t = tile_at(i, mt, nt);
+            const int b = (int)(n & 1);
+            const int row = t.m * C::BM + q * 32 + lane, n0 = t.n * C::BN;
+            const float as = row < p.M ? p.as[row] : 0.f;
+            if (et < C::BN) {
+                const int j = n0 + et;
+                sc[b][et] = j < p.N ? make_float2(p.bs[j], bias_at(p, j)) : make_float2(0.f, 0.f);
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(C::EPI * 32) : "memory");
+            // after a timeout the warp still meets the others at the barrier above, without work
+            if (ok) ok = tc::mbar_wait(&tfull[b], (uint32_t)(n / 2) & 1u, p.st);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                continue;
+            }
+            tc::fence_after_sync();
+            for (int c0 = half * (C::BN / 2); c0 < (half + 1) * (C::BN / 2) && n0 + c0 < p.N; c0 += cols) {
+                const uint32_t tad = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::BN + c0);
+                // the previous store has read the staging
+                if (TMA_OUT && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && !p.out_bf16) break;
+                    uint32_t v[32];
+                    tc::tmem_ld32_nw(tad + h * 32, v);
+                    tc::tmem_wait_ld();
+                    float o[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float4 s2 = *reinterpret_cast<const float4 *>(&sc[b][c0 + h * 32 + j]);
+                        o[j] = fmaf((float)(int)v[j] * as, s2.x, s2.y);
+                        o[j + 1] = fmaf((float)(int)v[j + 1] * as, s2.z, s2.w);
+                    }
+                    if (p.out_bf16) {
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __nv_bfloat162 x = __floats2bfloat162_rn(o[ch * 8 + 2 * j], o[ch * 8 + 2 * j + 1]);
+                                w[j] = *reinterpret_cast<const uint32_t *>(&x);
+                            }
+                            *reinterpret_cast<uint4 *>(slab + lane * 128 + (((h * 4 + ch) ^ (lane & 7)) * 16)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int ch = 0; ch < 8; ++ch)
+                            *reinterpret_cast<float4 *>(slab + lane * 128 + ((ch ^ (lane & 7)) * 16)) =
+                                make_float4(o[ch * 4], o[ch * 4 + 1], o[ch * 4 + 2], o[ch * 4 + 3]);
+                    }
+                }
+                const int r0 = t.m * C::BM + q * 32;
+                if (TMA_OUT) {
+                    tc::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && r0 < p.M) {
+                        asm volatile(
+                            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&to),
+                            "r"(n0 + c0), "r"(r0), "r"(tc::smem_u32(slab))
+                            : "memory");
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                } else {
+                    // rows off the 16-byte grid: element by element, whole rows of the slab
+                    __syncwarp();
+                    const int nc = min(cols, p.N - n0 - c0), nr = min(32, p.M - r0);
+                    for (int r = 0; r < nr; ++r)
+                        for (int j = lane; j < nc; j += 32) {
+                            const int64_t at = (int64_t)(r0 + r) * p.ldo + n0 + c0 + j;
+                            if (p.out_bf16)
+                                static_cast<__nv_bfloat16 *>(p.out)[at] = *reinterpret_cast<const __nv_bfloat16 *>(
+                                    slab + r * 128 + (((j >> 3) ^ (r & 7)) * 16) + (j & 7) * 2);
+                            else
+                                static_cast<float *>(p.out)[at] = *reinterpret_cast<const float *>(
+                                    slab + r * 128 + (((j >> 2) ^ (r & 7)) * 16) + (j & 3) * 4);
+                        }
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&tempty[b]);
+        }
+        // the staging outlives the stores' reads; the writes complete with the kernel
+        if (TMA_OUT && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc(tbase, 2 * C::BN);
+}
+
+// ---------------------------------------------------------------- few tokens or few tiles
+// BT tokens (TMEM columns) x 128 channels (lanes) per cluster of CTAs that
+// split the depth.
+template <int BT>
+struct Split {
+    static constexpr int NS = BT <= 32 ? 5 : 4;
+    static constexpr uint32_t W = 128 * 128, X = BT * 128, STAGE = W + X;
+    static constexpr int PITCH = 129;                                     // words per token of the partial sums
+    static constexpr uint32_t RING = NS * STAGE, PART = BT * PITCH * 4;
+    static constexpr size_t SMEM = (RING > PART ? RING : PART) + 1024;
+    static constexpr int TCOLS = BT < 32 ? 32 : BT;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int ld_cluster(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(128)
+    split_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const Args p,
+                 const int splits) {
+    using C = Split<BT>;
+    extern __shared__ uint8_t smraw[];
+    __shared__ uint64_t full[C::NS], empty[C::NS], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ int s_ok;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (tc::smem_u32(smraw) + 1023u) & ~1023u;
+    int *const part = reinterpret_cast<int *>(smraw + (base - tc::smem_u32(smraw)));
+    const uint32_t rank = splits > 1 ? cluster_rank() : 0;
+    const int n0 = (int)(blockIdx.x / splits) * 128, m0 = blockIdx.y * BT;
+    const int ks = (p.K + 127) / 128;
+    const int k0 = (int)((int64_t)ks * rank / splits), k1 = (int)((int64_t)ks * (rank + 1) / splits);
+    if (warp == 0) tc::tmem_alloc(&tmem_base, C::TCOLS);
+    if (tid == 0) {
+        for (int i = 0; i < C::NS; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        tc::mbar_init(&done, 1);
+        tc::fence_mbar_init();
+        s_ok = 1;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tbase = tmem_base;
+
+    if (tid == 0) {
+        // one thread loads ahead and issues the MMAs
+        constexpr uint32_t idesc = tc::idesc_i8(128, BT);
+        auto load = [&](int k) {
+            const int s = (k - k0) % C::NS;
+            const uint32_t sw = base + s * C::STAGE;
+            tc::mbar_arrive_expect_tx(&full[s], C::STAGE);
+            tc::tma_load_2d(sw, &tw, &full[s], k * 128, n0);
+            tc::tma_load_2d(sw + C::W, &tx, &full[s], k * 128, m0);
+        };
+        int issued = k0;
+        for (; issued < k1 && issued < k0 + C::NS; ++issued) load(issued);
+        bool ok = true;
+        for (int k = k0; k < k1; ++k) {
+            const int c = k - k0, s = c % C::NS;
+            if (!(ok = tc::mbar_wait(&full[s], (uint32_t)(c / C::NS) & 1u, p.st))) break;
+            tc::fence_after_sync();
+            const uint32_t sw = base + s * C::STAGE;
+            mma_stage(tbase, sw, sw + C::W, idesc, p.K - k * 128, c == 0);
+            tc::mma_commit(&empty[s]);
+            // refill the stage of the step before, whose MMAs run ahead of these
+            if (c >= 1 && issued < k1) {
+                const int s1 = (c - 1) % C::NS;
+                if (!(ok = tc::mbar_wait(&empty[s1], (uint32_t)((c - 1) / C::NS) & 1u, p.st))) break;
+                load(issued++);
+            }
+        }
+        tc::mma_commit(&done);
+        ok &= tc::mbar_wait(&done, 0, p.st);
+        if (!ok) {
+            // copies issued but not consumed land before the shared memory is reused
+            for (int k = max(k0, issued - C::NS); k < issued; ++k)
+                tc::mbar_wait(&full[(k - k0) % C::NS], (uint32_t)((k - k0) / C::NS) & 1u, p.st);
+            s_ok = 0;
+        }
+    }
+    __syncthreads();
+    tc::fence_after_sync();
+    const int nl = tid, n = n0 + nl;                    // this thread's channel
+    const int rows = min(BT, p.M - m0);
+    const float bs = n < p.N ? p.bs[n] : 0.f, bias = n < p.N ? bias_at(p, n) : 0.f;
+    auto put = [&](int m, int sum) {
+        if (n >= p.N) return;
+        const float v = fmaf((float)sum * p.as[m0 + m], bs, bias);
+        const int64_t at = (int64_t)(m0 + m) * p.ldo + n;
+        if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
+        else static_cast<float *>(p.out)[at] = v;
+    };
+    const bool ok = s_ok != 0;
+    if (splits == 1) {
+        for (int c0 = 0; c0 < rows && ok; c0 += 16) {
+            uint32_t v[16];
+            tc::tmem_ld16_nw(tbase + ((uint32_t)(warp * 32) << 16) + c0, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c0 + j < rows) put(c0 + j, p.K ? (int)v[j] : 0);
+        }
+    } else {
+        for (int c0 = 0; c0 < rows; c0 += 16) {
+            uint32_t v[16];
+            tc::tmem_ld16_nw(tbase + ((uint32_t)(warp * 32) << 16) + c0, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) part[(c0 + j) * C::PITCH + nl] = (int)v[j];
+        }
+        cluster_sync();
+        for (int m = (int)rank; m < rows && ok; m += splits) {
+            int sum = 0;
+            for (int r = 0; r < splits; ++r) sum += ld_cluster(base + (uint32_t)(m * C::PITCH + nl) * 4u, r);
+            put(m, sum);
+        }
+        cluster_sync();                                  // the others have read this CTA's sums
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(tbase, C::TCOLS);
+}
+
+template <int BT>
+dbc_status launch_split(const int8_t *a, int64_t lda, const int8_t *b, int64_t ldb, const Args &p, cudaStream_t st) {
+    using C = Split<BT>;
+    CUtensorMap tw, tx;
+    memset(&tw, 0, sizeof tw);
+    memset(&tx, 0, sizeof tx);
+    if (p.K && (!tma::encode_i8_rows(&tw, b, p.N, p.K, ldb, 128) || !tma::encode_i8_rows(&tx, a, p.M, p.K, lda, BT)))
+        return DBC_ERR_CUDA;
+    const int nt = (p.N + 127) / 128, mt = (p.M + BT - 1) / BT, ks = (p.K + 127) / 128;
+    int splits = 1;
+    while (splits < 8 && splits * 4 <= ks && (int64_t)nt * mt * splits * 2 <= 296) splits *= 2;
+    if (cudaFuncSetAttribute(split_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) !=
+        cudaSuccess)
+        return DBC_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(nt * splits), (unsigned)mt);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)splits;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, split_kernel<BT>, tw, tx, p, splits) != cudaSuccess) return DBC_ERR_CUDA;
+    return DBC_OK;
+}
+
+dbc_status launch_wide(const int8_t *a, int64_t lda, const int8_t *b, int64_t ldb, const Args &p, cudaStream_t st) {
+    using C = Wide;
+    CUtensorMap ta, tb, to;
+    memset(&to, 0, sizeof to);
+    if (!tma::encode_i8_rows(&ta, a, p.M, p.K, lda, C::BM) || !tma::encode_i8_rows(&tb, b, p.N, p.K, ldb, C::BN))
+        return DBC_ERR_CUDA;
+    const int64_t esz = p.out_bf16 ? 2 : 4;
+    const bool tma_out = aligned16(p.out) && p.ldo * esz % 16 == 0 &&
+                         tma::encode_out_rows(&to, p.out, p.out_bf16, p.M, p.N, p.ldo, 32);
+    auto *k = tma_out ? wide_kernel<true> : wide_kernel<false>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
+        return DBC_ERR_CUDA;
+    const int64_t tiles = (int64_t)((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
+    k<<<(unsigned)std::min<int64_t>(tiles, num_sms()), C::THREADS, C::SMEM, st>>>(ta, tb, to, p);
+    return DBC_OK;
 }
 
 }  // namespace mi
@@ -93,10 +464,17 @@ extern "C" dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_sca
     if ((reinterpret_cast<uintptr_t>(out) % oa) || (bias && reinterpret_cast<uintptr_t>(bias) % ba) ||
         (reinterpret_cast<uintptr_t>(a_scale) % 4) || (reinterpret_cast<uintptr_t>(b_scale) % 4))
         return DBC_ERR_INVALID_ARG;
-    const mi::Args p{a, b, a_scale, b_scale, bias, out, lda, ldb, ldo, M, N, (int)K, bias_dtype == DBC_BF16,
+    const mi::Args p{a_scale, b_scale, bias, out, ldo, (int)M, (int)N, (int)K, bias_dtype == DBC_BF16,
                      out_dtype == DBC_BF16, dev_status};
-    const dim3 grid((unsigned)((M + 63) / 64), (unsigned)std::min<int64_t>((N + 63) / 64, 32768));
-    mi::dot_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t wide_tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    dbc_status c;
+    if (K > 0 && M > 128 && wide_tiles >= 148) c = mi::launch_wide(a, lda, b, ldb, p, st);
+    else if (M <= 16) c = mi::launch_split<16>(a, lda, b, ldb, p, st);
+    else if (M <= 32) c = mi::launch_split<32>(a, lda, b, ldb, p, st);
+    else if (M <= 64) c = mi::launch_split<64>(a, lda, b, ldb, p, st);
+    else c = mi::launch_split<128>(a, lda, b, ldb, p, st);
+    if (c != DBC_OK) return c;
     count_launches(1);
     return launch_status();
 }

@@ -60,5 +60,37 @@ inline bool encode_f32_rows(CUtensorMap *map, const void *base, uint64_t rows, u
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map of row-major 8-bit rows of K bytes, `ld` bytes apart (a multiple of 16, base 16-byte
+// aligned), read in boxes of box_rows x 128 bytes with the 128-byte swizzle.  Bytes past K and rows
+// past the end read as zeros.
+inline bool encode_i8_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t K, uint64_t ld,
+                           uint32_t box_rows) {
+    EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {K, rows};
+    const cuuint64_t strides[1] = {ld};
+    const cuuint32_t box[2] = {128, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor map of row-major fp32 or bf16 rows of `cols` elements, `ld` elements apart (row starts on
+// 16-byte boundaries), for tile stores of box_rows x 128 bytes with the 128-byte swizzle.
+inline bool encode_out_rows(CUtensorMap *map, void *base, bool bf16, uint64_t rows, uint64_t cols, uint64_t ld,
+                            uint32_t box_rows) {
+    EncodeFn fn = encoder();
+    if (!fn) return false;
+    const uint32_t esz = bf16 ? 2 : 4;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {ld * esz};
+    const cuuint32_t box[2] = {128 / esz, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace tma
 }  // namespace dbc
