@@ -4,10 +4,12 @@
 // Both kernels feed kind::i8 tcgen05 MMAs (128 x N x 32 per instruction, sums
 // in TMEM) from a ring of TMA-loaded, 128-byte swizzled stages of 128 bytes of
 // K; TMA's zero fill pads odd depths and row counts.
-//   * wide_kernel: 128 tokens x 128 channels per tile, one persistent CTA per
-//     SM; loads, MMAs and the epilogue of the previous tile (two accumulators)
-//     run at the same time.  Outputs leave through swizzled staging and TMA tile
-//     stores.
+//   * wide_kernel: 256 tokens x 256 channels per tile and pair of CTAs
+//     (cta_group::2: each CTA loads half of both operands, so that a byte of
+//     shared memory feeds twice the products of a single CTA's tile), one
+//     persistent CTA per SM; loads, MMAs and the epilogue of the tile before (two
+//     accumulators) run at the same time.  Outputs leave through swizzled staging
+//     and TMA tile stores.
 //   * split_kernel: for few tokens or few tiles.  128 CHANNELS sit on the TMEM
 //     lanes and the tokens on its columns, so that one token costs 16 columns
 //     and not 128 lanes; the depth is split over a cluster of up to 8 CTAs,
@@ -18,6 +20,7 @@
 #include <cuda.h>
 #include <string.h>
 
+#include "pairs.cuh"
 #include "tc.cuh"
 #include "tma_host.cuh"
 
@@ -53,10 +56,10 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sa, uint32_t sb, 
 
 // ---------------------------------------------------------------- many tiles
 struct Wide {
-    static constexpr int BM = 128, BN = 128, NS = 5, EPI = 8;             // EPI epilogue warps
-    static constexpr int THREADS = 64 + EPI * 32;
-    static constexpr uint32_t A = BM * 128, B = BN * 128, STAGE = A + B;
-    static constexpr uint32_t SLAB = 32 * 128;                            // one warp's rows x 128 bytes
+    static constexpr int BM = 256, BN = 256;                              // of a pair; each CTA loads half of both
+    static constexpr int NS = 5, EPI = 16, THREADS = 64 + EPI * 32;
+    static constexpr uint32_t HALF = 128 * 128, STAGE = 2 * HALF;
+    static constexpr uint32_t SLAB = 32 * 64;                             // one warp's 32 rows x 64 bytes
     static constexpr size_t SMEM = NS * STAGE + EPI * SLAB + 1024;
 };
 
@@ -73,27 +76,30 @@ __device__ __forceinline__ Tile tile_at(int64_t i, int mt, int nt) {
     return {(int)(rem / w), g * 16 + (int)(rem % w)};
 }
 
-template <bool TMA_OUT>
-__global__ void __launch_bounds__(Wide::THREADS, 1)
+template <bool TMA_OUT, bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const __grid_constant__ CUtensorMap to, const Args p) {
     using C = Wide;
     extern __shared__ uint8_t smraw[];
+    // full: CTA 0's, both producers' copies; empty, tfull: each CTA's, committed by CTA 0's MMAs;
+    // tempty: CTA 0's, the epilogue warps of both CTAs
     __shared__ uint64_t full[C::NS], empty[C::NS], tfull[2], tempty[2], drain;
     __shared__ uint32_t tmem_base;
-    __shared__ __align__(16) float2 sc[2][C::BN];      // per channel: scale, bias
+    __shared__ __align__(16) float s_scale[2][C::BN], s_bias[2][C::BN];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = tc::cluster_rank();
     const uint32_t base = (tc::smem_u32(smraw) + 1023u) & ~1023u;
     uint8_t *const sgen = smraw + (base - tc::smem_u32(smraw));
-    if (warp == 1) tc::tmem_alloc(&tmem_base, 2 * C::BN);
+    if (warp == 1) tc::tmem_alloc_pair(&tmem_base, 2 * C::BN);
     if (tid == 0) {
         for (int i = 0; i < C::NS; ++i) {
-            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&full[i], 2);
             tc::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&tfull[i], 1);
-            tc::mbar_init(&tempty[i], C::EPI);
+            tc::mbar_init(&tempty[i], 2 * C::EPI);
         }
         tc::mbar_init(&drain, 1);
         tc::fence_mbar_init();
@@ -103,156 +109,213 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
     }
     tc::fence_before_sync();
     __syncthreads();
+    tc::cluster_sync();                                  // both CTAs' barriers exist
     tc::fence_after_sync();
     const uint32_t tbase = tmem_base;
     const int mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN, ks = (p.K + 127) / 128;
-    const int64_t tiles = (int64_t)mt * nt;
+    const int64_t tiles = (int64_t)mt * nt, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
 
     if (warp == 0) {
         if (lane == 0) {
-            int s = 0, issued = 0;                       // stage; copies since the start, up to NS
+            int s = 0, issued = 0;                       // stage; stages in use, up to NS
             uint32_t ph = 1;                             // parity of the stage's last release
             bool ok = true;
-            for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+            for (int64_t i = pair; i < tiles && ok; i += pairs) {
                 const Tile t = tile_at(i, mt, nt);
+                const int y0 = t.m * C::BM + (int)rank * 128, x0 = t.n * C::BN + (int)rank * 128;
                 for (int k = 0; k < ks; ++k) {
                     if (issued == C::NS && !(ok = tc::mbar_wait(&empty[s], ph, p.st))) break;
                     issued += issued < C::NS;
-                    const uint32_t sa = base + s * C::STAGE;
-                    tc::mbar_arrive_expect_tx(&full[s], C::STAGE);
-                    tc::tma_load_2d(sa, &ta, &full[s], k * 128, t.m * C::BM);
-                    tc::tma_load_2d(sa + C::A, &tb, &full[s], k * 128, t.n * C::BN);
+                    const uint32_t sa = base + s * C::STAGE, bar = tc::map_to(tc::smem_u32(&full[s]), 0);
+                    tc::mbar_arrive_expect_tx_at(bar, C::STAGE);
+                    tc::tma_load_2d_pair(sa, &ta, bar, k * 128, y0);
+                    tc::tma_load_2d_pair(sa + C::HALF, &tb, bar, k * 128, x0);
                     if (++s == C::NS) s = 0, ph ^= 1;
                 }
             }
-            // after a timeout: every stage's last copies land before the CTA ends
+            // all stages released: no arrival is under way to a CTA that has ended
+            for (int k = 0; k < issued && ok; ++k) {
+                const bool wrap = issued == C::NS && s + k >= C::NS;
+                ok = issued == C::NS ? tc::mbar_wait(&empty[wrap ? s + k - C::NS : s + k], wrap ? ph ^ 1 : ph, p.st)
+                                     : tc::mbar_wait(&empty[k], 0, p.st);
+            }
+            // after a timeout: copies under way (microseconds) land before the CTA ends
             if (!ok)
-                for (int k = 0; k < C::NS; ++k) tc::mbar_wait(&full[k], k < s ? ph ^ 1 : ph, p.st);
+                for (const long long t0 = clock64(); clock64() - t0 < (1ll << 22);) {
+                }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (rank == 0) {
+            // The whole warp walks the loop and one elected lane issues: descriptors stay in uniform
+            // registers (issued from a single-lane branch an MMA took 80 cycles, its work takes 128).
+            // The next stage's barrier is asked before this stage's MMAs are issued.
             constexpr uint32_t idesc = tc::idesc_i8(C::BM, C::BN);
+            const bool issuer = tc::elect_one();
             int s = 0;
             uint32_t ph = 0;
             int64_t n = 0;
-            bool ok = true;
-            for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x, ++n) {
+            bool ok = true, ready = false;
+            for (int64_t i = pair; i < tiles && ok; i += pairs, ++n) {
                 const int b = (int)(n & 1);
-                if (n >= 2 && !(ok = tc::mbar_wait(&tempty[b], (uint32_t)(n / 2 - 1) & 1u, p.st))) break;
-                tc::fence_after_sync();
+                if (n >= 2) ok = tc::mbar_wait(&tempty[b], (uint32_t)(n / 2 - 1) & 1u, p.st);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 for (int k = 0; k < ks; ++k) {
-                    if (!(ok = tc::mbar_wait(&full[s], ph, p.st))) break;
+                    if (!ready) ok = tc::mbar_wait(&full[s], ph, p.st);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const int s1 = s + 1 == C::NS ? 0 : s + 1;
+                    const uint32_t ph1 = s + 1 == C::NS ? ph ^ 1 : ph;
+                    ready = tc::mbar_try_wait(&full[s1], ph1);
                     tc::fence_after_sync();
                     const uint32_t sa = base + s * C::STAGE;
-                    mma_stage(tbase + b * C::BN, sa, sa + C::A, idesc, p.K - k * 128, k == 0);
-                    tc::mma_commit(&empty[s]);
-                    if (++s == C::NS) s = 0, ph ^= 1;
+                    const uint64_t da = tc::sdesc(sa, 16, 1024), db = tc::sdesc(sa + C::HALF, 16, 1024);
+                    const int left = p.K - k * 128;
+                    if (issuer) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j * 32 < left)
+                                tc::mma_i8_pair(tbase + b * C::BN, tc::sdesc_add(da, j * 32), tc::sdesc_add(db, j * 32),
+                                                idesc, k || j ? 1u : 0u);
+                        tc::mma_commit_pair(&empty[s]);
+                    }
+                    __syncwarp();
+                    s = s1, ph = ph1;
                 }
-                if (ok) tc::mma_commit(&tfull[b]);
+                if (ok && issuer) tc::mma_commit_pair(&tfull[b]);
+                __syncwarp();
             }
             if (!ok) {
-                tc::mma_commit(&drain);
-                tc::mbar_wait(&drain, 0, p.st);
+                if (issuer) {
+                    tc::mma_commit_pair(&drain);
+                    tc::mbar_wait(&drain, 0, p.st);
+                }
+                __syncwarp();
             }
         }
     } else {
-        // warp w reads TMEM lanes (w % 4) * 32 .. + 31 and one half of the columns
-        const int q = warp & 3, half = (warp - 2) >> 2, et = tid - 64;
+        // Warp w owns TMEM lanes (w % 4) * 32 .. + 31 (its tokens) and 64 of the 256 columns.  It takes
+        // them into registers at once and releases the accumulator, so that the MMAs of the tile
+        // after next do not wait for the arithmetic.
+        const int q = warp & 3, cg = ((warp - 2) >> 2) * 64, et = tid - 64;
         uint8_t *const slab = sgen + C::NS * C::STAGE + (warp - 2) * C::SLAB;
-        const int cols = p.out_bf16 ? 64 : 32;           // columns of a slab
-        int64_t n = 0;
+        const uint32_t release[2] = {tc::map_to(tc::smem_u32(&tempty[0]), 0), tc::map_to(tc::smem_u32(&tempty[1]), 0)};
+        constexpr int COLS = BF16 ? 32 : 16;             // columns of a slab
+        constexpr int E = COLS / 4;                      // elements of 16 bytes
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x, ++n) {
+        // The next tile's scales are fetched while this one is computed: the row's by its thread, the
+        // channels' scales by the first 256 threads, their bias by the others.
+        float as = 0.f;
+        uint32_t ch_raw = 0;
+        auto fetch = [&](int64_t i) {
+            if (i >= tiles) return;
             const Tile t = tile_at(i, mt, nt);
-            const int b = (int)(n & 1);
-            const int row = t.m * C::BM + q * 32 + lane, n0 = t.n * C::BN;
-            const float as = row < p.M ? p.as[row] : 0.f;
-            if (et < C::BN) {
-                const int j = n0 + et;
-                sc[b][et] = j < p.N ? make_float2(p.bs[j], bias_at(p, j)) : make_float2(0.f, 0.f);
+            const int row = t.m * C::BM + (int)rank * 128 + q * 32 + lane, j = t.n * C::BN + (et & 255);
+            if (row < p.M) as = p.as[row];
+            if (j < p.N) {
+                if (et < 256) ch_raw = __float_as_uint(p.bs[j]);
+                else if (p.bias && p.bias_bf16) ch_raw = static_cast<const uint16_t *>(p.bias)[j];
+                else if (p.bias) ch_raw = static_cast<const uint32_t *>(p.bias)[j];
             }
+        };
+        fetch(pair);
+        int b = 0;
+        uint32_t ph = 0;
+        for (int64_t i = pair; i < tiles; i += pairs, ph ^= b, b ^= 1) {
+            const Tile t = tile_at(i, mt, nt);
+            const int r0 = t.m * C::BM + (int)rank * 128 + q * 32, n0 = t.n * C::BN + cg;
+            // the other buffer is still read by warps of the tile before; this one's readers are past the
+            // barrier of that tile
+            if (et < 256) s_scale[b][et] = __uint_as_float(ch_raw);
+            else s_bias[b][et - 256] = __uint_as_float(p.bias_bf16 ? ch_raw << 16 : ch_raw);
+            const float2 as2 = make_float2(as, as);
             asm volatile("bar.sync 1, %0;" ::"n"(C::EPI * 32) : "memory");
-            // after a timeout the warp still meets the others at the barrier above, without work
-            if (ok) ok = tc::mbar_wait(&tfull[b], (uint32_t)(n / 2) & 1u, p.st);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                continue;
-            }
+            fetch(i + pairs);
+            // after a timeout the warps still meet at the barrier above, without work
+            if (ok && lane == 0) ok = tc::mbar_wait(&tfull[b], ph, p.st);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) continue;
             tc::fence_after_sync();
-            for (int c0 = half * (C::BN / 2); c0 < (half + 1) * (C::BN / 2) && n0 + c0 < p.N; c0 += cols) {
-                const uint32_t tad = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::BN + c0);
-                // the previous store has read the staging
-                if (TMA_OUT && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                __syncwarp();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && !p.out_bf16) break;
-                    uint32_t v[32];
-                    tc::tmem_ld32_nw(tad + h * 32, v);
-                    tc::tmem_wait_ld();
-                    float o[32];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float4 s2 = *reinterpret_cast<const float4 *>(&sc[b][c0 + h * 32 + j]);
-                        o[j] = fmaf((float)(int)v[j] * as, s2.x, s2.y);
-                        o[j + 1] = fmaf((float)(int)v[j + 1] * as, s2.z, s2.w);
-                    }
-                    if (p.out_bf16) {
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const __nv_bfloat162 x = __floats2bfloat162_rn(o[ch * 8 + 2 * j], o[ch * 8 + 2 * j + 1]);
-                                w[j] = *reinterpret_cast<const uint32_t *>(&x);
-                            }
-                            *reinterpret_cast<uint4 *>(slab + lane * 128 + (((h * 4 + ch) ^ (lane & 7)) * 16)) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int ch = 0; ch < 8; ++ch)
-                            *reinterpret_cast<float4 *>(slab + lane * 128 + ((ch ^ (lane & 7)) * 16)) =
-                                make_float4(o[ch * 4], o[ch * 4 + 1], o[ch * 4 + 2], o[ch * 4 + 3]);
-                    }
-                }
-                const int r0 = t.m * C::BM + q * 32;
-                if (TMA_OUT) {
-                    tc::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && r0 < p.M) {
-                        asm volatile(
-                            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&to),
-                            "r"(n0 + c0), "r"(r0), "r"(tc::smem_u32(slab))
-                            : "memory");
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    }
-                } else {
-                    // rows off the 16-byte grid: element by element, whole rows of the slab
-                    __syncwarp();
-                    const int nc = min(cols, p.N - n0 - c0), nr = min(32, p.M - r0);
-                    for (int r = 0; r < nr; ++r)
-                        for (int j = lane; j < nc; j += 32) {
-                            const int64_t at = (int64_t)(r0 + r) * p.ldo + n0 + c0 + j;
-                            if (p.out_bf16)
-                                static_cast<__nv_bfloat16 *>(p.out)[at] = *reinterpret_cast<const __nv_bfloat16 *>(
-                                    slab + r * 128 + (((j >> 3) ^ (r & 7)) * 16) + (j & 7) * 2);
-                            else
-                                static_cast<float *>(p.out)[at] = *reinterpret_cast<const float *>(
-                                    slab + r * 128 + (((j >> 2) ^ (r & 7)) * 16) + (j & 3) * 4);
-                        }
-                }
-            }
+            uint32_t v[2][32];
+            const uint32_t tad = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::BN + cg);
+            tc::tmem_ld32_nw(tad, v[0]);
+            tc::tmem_ld32_nw(tad + 32, v[1]);
+            tc::tmem_wait_ld();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&tempty[b]);
+            if (lane == 0) tc::mbar_arrive_at(release[b]);
+            if (n0 >= p.N || r0 >= p.M) continue;
+#pragma unroll
+            for (int c0 = 0; c0 < 64; c0 += COLS) {
+                if (TMA_OUT && lane == 0)                // the store before has read the staging
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {         // 16 bytes of this thread's row
+                    float o[E];
+#pragma unroll
+                    for (int j = 0; j < E; j += 4) {
+                        const int c = c0 + ch * E + j;
+                        const float4 s4 = *reinterpret_cast<const float4 *>(&s_scale[b][cg + c]);
+                        const float4 b4 = *reinterpret_cast<const float4 *>(&s_bias[b][cg + c]);
+                        const uint32_t *x = &v[c >> 5][c & 31];
+                        const float2 lo = fma2(mul2(make_float2((float)(int)x[0], (float)(int)x[1]), as2),
+                                               make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
+                        const float2 hi = fma2(mul2(make_float2((float)(int)x[2], (float)(int)x[3]), as2),
+                                               make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
+                        o[j] = lo.x, o[j + 1] = lo.y, o[j + 2] = hi.x, o[j + 3] = hi.y;
+                    }
+                    uint4 w;
+                    if constexpr (BF16) {
+                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(o[0], o[1]), h1 = __floats2bfloat162_rn(o[2], o[3]);
+                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[4], o[5]), h3 = __floats2bfloat162_rn(o[6], o[7]);
+                        w = make_uint4(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1),
+                                       *reinterpret_cast<const uint32_t *>(&h2), *reinterpret_cast<const uint32_t *>(&h3));
+                    } else {
+                        w = make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
+                                       __float_as_uint(o[3]));
+                    }
+                    // 64-byte swizzle: chunk c of row r at c ^ (r / 2 % 4)
+                    *reinterpret_cast<uint4 *>(slab + lane * 64 + ((ch ^ ((lane >> 1) & 3)) * 16)) = w;
+                }
+                if (n0 + c0 < p.N) {
+                    if (TMA_OUT) {
+                        tc::fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            asm volatile(
+                                "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                                    &to),
+                                "r"(n0 + c0), "r"(r0), "r"(tc::smem_u32(slab))
+                                : "memory");
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        }
+                    } else {
+                        // output rows off the 16-byte grid: element by element, row after row of the slab
+                        __syncwarp();
+                        const int cols = min(COLS, p.N - n0 - c0), rows = min(32, p.M - r0);
+                        constexpr int STEP = 32 / COLS;  // rows at a time
+                        const int j = lane % COLS;
+                        for (int r = lane / COLS; r < rows; r += STEP) {
+                            if (j >= cols) continue;
+                            const int64_t at = (int64_t)(r0 + r) * p.ldo + n0 + c0 + j;
+                            const uint8_t *src = slab + r * 64 + (((j / E) ^ ((r >> 1) & 3)) * 16);
+                            if constexpr (BF16)
+                                static_cast<__nv_bfloat16 *>(p.out)[at] =
+                                    reinterpret_cast<const __nv_bfloat16 *>(src)[j % E];
+                            else
+                                static_cast<float *>(p.out)[at] = reinterpret_cast<const float *>(src)[j % E];
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
         }
         // the staging outlives the stores' reads; the writes complete with the kernel
         if (TMA_OUT && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 1) tc::tmem_dealloc(tbase, 2 * C::BN);
+    tc::cluster_sync();                                  // nothing of the pair is under way to this CTA
+    if (warp == 1) tc::tmem_dealloc_pair(tbase, 2 * C::BN);
 }
 
 // ---------------------------------------------------------------- few tokens or few tiles
@@ -268,20 +331,9 @@ struct Split {
     static constexpr int TCOLS = BT < 32 ? 32 : BT;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ int ld_cluster(uint32_t addr, uint32_t rank) {
-    uint32_t a;
     int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(tc::map_to(addr, rank)) : "memory");
     return v;
 }
 
@@ -297,7 +349,7 @@ __global__ void __launch_bounds__(128)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (tc::smem_u32(smraw) + 1023u) & ~1023u;
     int *const part = reinterpret_cast<int *>(smraw + (base - tc::smem_u32(smraw)));
-    const uint32_t rank = splits > 1 ? cluster_rank() : 0;
+    const uint32_t rank = splits > 1 ? tc::cluster_rank() : 0;
     const int n0 = (int)(blockIdx.x / splits) * 128, m0 = blockIdx.y * BT;
     const int ks = (p.K + 127) / 128;
     const int k0 = (int)((int64_t)ks * rank / splits), k1 = (int)((int64_t)ks * (rank + 1) / splits);
@@ -382,13 +434,13 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
             for (int j = 0; j < 16; ++j) part[(c0 + j) * C::PITCH + nl] = (int)v[j];
         }
-        cluster_sync();
+        tc::cluster_sync();
         for (int m = (int)rank; m < rows && ok; m += splits) {
             int sum = 0;
             for (int r = 0; r < splits; ++r) sum += ld_cluster(base + (uint32_t)(m * C::PITCH + nl) * 4u, r);
             put(m, sum);
         }
-        cluster_sync();                                  // the others have read this CTA's sums
+        tc::cluster_sync();                                  // the others have read this CTA's sums
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -428,16 +480,17 @@ dbc_status launch_wide(const int8_t *a, int64_t lda, const int8_t *b, int64_t ld
     using C = Wide;
     CUtensorMap ta, tb, to;
     memset(&to, 0, sizeof to);
-    if (!tma::encode_i8_rows(&ta, a, p.M, p.K, lda, C::BM) || !tma::encode_i8_rows(&tb, b, p.N, p.K, ldb, C::BN))
+    if (!tma::encode_i8_rows(&ta, a, p.M, p.K, lda, 128) || !tma::encode_i8_rows(&tb, b, p.N, p.K, ldb, 128))
         return DBC_ERR_CUDA;
     const int64_t esz = p.out_bf16 ? 2 : 4;
     const bool tma_out = aligned16(p.out) && p.ldo * esz % 16 == 0 &&
                          tma::encode_out_rows(&to, p.out, p.out_bf16, p.M, p.N, p.ldo, 32);
-    auto *k = tma_out ? wide_kernel<true> : wide_kernel<false>;
+    auto *k = tma_out ? (p.out_bf16 ? wide_kernel<true, true> : wide_kernel<true, false>)
+                      : (p.out_bf16 ? wide_kernel<false, true> : wide_kernel<false, false>);
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
         return DBC_ERR_CUDA;
     const int64_t tiles = (int64_t)((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
-    k<<<(unsigned)std::min<int64_t>(tiles, num_sms()), C::THREADS, C::SMEM, st>>>(ta, tb, to, p);
+    k<<<(unsigned)(2 * std::min<int64_t>(tiles, num_sms() / 2)), C::THREADS, C::SMEM, st>>>(ta, tb, to, p);
     return DBC_OK;
 }
 
@@ -467,9 +520,9 @@ extern "C" dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_sca
     const mi::Args p{a_scale, b_scale, bias, out, ldo, (int)M, (int)N, (int)K, bias_dtype == DBC_BF16,
                      out_dtype == DBC_BF16, dev_status};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t wide_tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    const int64_t wide_tiles = ((M + 255) / 256) * ((N + 255) / 256);
     dbc_status c;
-    if (K > 0 && M > 128 && wide_tiles >= 148) c = mi::launch_wide(a, lda, b, ldb, p, st);
+    if (K > 0 && M > 128 && wide_tiles >= 37) c = mi::launch_wide(a, lda, b, ldb, p, st);
     else if (M <= 16) c = mi::launch_split<16>(a, lda, b, ldb, p, st);
     else if (M <= 32) c = mi::launch_split<32>(a, lda, b, ldb, p, st);
     else if (M <= 64) c = mi::launch_split<64>(a, lda, b, ldb, p, st);

@@ -77,7 +77,8 @@ inline bool encode_i8_rows(CUtensorMap *map, const void *base, uint64_t rows, ui
 }
 
 // Tensor map of row-major fp32 or bf16 rows of `cols` elements, `ld` elements apart (row starts on
-// 16-byte boundaries), for tile stores of box_rows x 128 bytes with the 128-byte swizzle.
+// 16-byte boundaries), for tile stores of box_rows x 64 bytes with the 64-byte swizzle (chunk c of row
+// r at c ^ (r / 2 % 4)).
 inline bool encode_out_rows(CUtensorMap *map, void *base, bool bf16, uint64_t rows, uint64_t cols, uint64_t ld,
                             uint32_t box_rows) {
     EncodeFn fn = encoder();
@@ -85,10 +86,10 @@ inline bool encode_out_rows(CUtensorMap *map, void *base, bool bf16, uint64_t ro
     const uint32_t esz = bf16 ? 2 : 4;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {ld * esz};
-    const cuuint32_t box[2] = {128 / esz, box_rows};
+    const cuuint32_t box[2] = {64 / esz, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides,
-              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
