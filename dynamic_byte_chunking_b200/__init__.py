@@ -130,9 +130,15 @@ def status_string(code: int) -> str:
 
 
 # ---------------------------------------------------------------- helpers
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -479,66 +485,80 @@ def chunk_coding_rate_canon(H, w, eps2: float, bias=None, *, offsets=None, T: Op
 
 
 # ---------------------------------------------------------------- residual norm and 8-bit products
-def _elsewhere(device, stream):
-    """The stream to make current first: a given one, or the tensors' device's when another is current."""
+# These calls are short enough for the host's part to show (a decoding step makes many of them), so the
+# common case (contiguous inputs on the current device, outputs made here) looks at little.
+def _elsewhere(stream, *ts):
+    """None when all tensors are on the current device and no stream is given; else the stream to make
+    current first (the given one, or the tensors' device's own)."""
     torch = _torch()
+    index = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != index:
+            if not t.is_cuda or index < 0:
+                raise ValueError("dbc kernels take CUDA tensors only (no CPU path)")
+            raise ValueError(f"tensors on {ts[0].device} and {t.device}: all have to be on one device")
+    if index < 0:
+        raise ValueError("dbc kernels take CUDA tensors only (no CPU path)")
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        if stream.device_index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {ts[0].device}")
         return stream
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.current_stream(device)
+    if index != torch.cuda.current_device():
+        return torch.cuda.current_stream(index)
     return None
 
 
-def _one_device(*ts):
-    device = ts[0].device
-    for t in ts:
-        if t is not None:
-            if not t.is_cuda:
-                raise ValueError("dbc kernels take CUDA tensors only (no CPU path)")
-            if t.device != device:
-                raise ValueError(f"tensors on {device} and {t.device}: all have to be on one device")
-    return device
+def _here(t) -> int:
+    """The current stream of t's device (the current one), as the library takes it."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # a Stream object costs 3 us to make
+    return raw(t.get_device()) if raw is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _like(t, dtype):
+    """A fresh contiguous tensor of t's shape."""
+    if t.dtype == dtype and t.is_contiguous():
+        return _torch().empty_like(t)
+    return t.new_empty(t.shape, dtype=dtype)
 
 
 def _code(t, what: str) -> int:
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    dtype = t.dtype
+    if dtype == torch.bfloat16:
         return DBC_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return DBC_F32
     raise TypeError(f"{what} must be bfloat16 or float32")
 
 
 def _status_word(t):
-    torch = _torch()
-    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+    if t is None:
+        return None
+    if t.dtype != _torch().int32 or t.numel() < 1:
         raise TypeError("dev_status must be an int32 tensor")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 def _rows_in(t, d: int):
-    """(t2, stride): t as [N, d] rows with unit inner stride; a view where its strides allow, else a copy."""
-    if t.dim() != 2:
-        t = t.reshape(-1, d)
-    N = t.shape[0]
-    if (d > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < d):
-        t = t.contiguous()
-    return t, (t.stride(0) if N > 1 else d)
+    """(t, stride): t as rows of d with unit inner stride; itself where its strides allow, else a copy."""
+    if t.is_contiguous():
+        return t, d
+    if t.dim() != 2 or (d > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < d):
+        return t.contiguous(), d
+    return t, (t.stride(0) if t.shape[0] > 1 else d)
 
 
 def _rows_out(t, shape, dtype, what: str):
     """Row stride of a caller's output buffer (its rows are written in place, so it must be a plain one)."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}")
     d = shape[-1]
-    if t.dim() != 2 and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous, or [N, d] with unit inner stride")
-    N = t.shape[0] if t.dim() == 2 else 1
-    if t.dim() == 2 and ((d > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < d)):
-        raise ValueError(f"{what} must have unit inner stride and a row stride of at least d")
-    return t.stride(0) if t.dim() == 2 and N > 1 else d
+    if t.is_contiguous():
+        return d
+    if t.dim() != 2 or (d > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < d):
+        raise ValueError(f"{what} must be contiguous, or [N, d] with unit inner stride and a row stride >= d")
+    return t.stride(0) if shape[0] > 1 else d
 
 
 def _weight_arg(weight, d: int):
@@ -548,51 +568,46 @@ def _weight_arg(weight, d: int):
     if weight.dim() != 1 or weight.shape[0] != d:
         raise ValueError(f"weight must have shape [{d}]")
     code = _code(weight, "weight")
-    weight = weight.contiguous()
-    return _ptr(weight), code, weight
+    if not weight.is_contiguous():
+        weight = weight.contiguous()
+    return weight.data_ptr(), code, weight
 
 
-def _norm_inputs(x, residual, weight):
+def _width(x, what: str) -> int:
     if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("x must be [..., d] with d >= 1")
-    d = x.shape[-1]
-    code = _code(x, "x")
-    x2, xs = _rows_in(x, d)
-    r2, rs = None, 0
-    if residual is not None:
-        if residual.shape != x.shape or residual.dtype != x.dtype:
-            raise ValueError("residual must have x's shape and dtype")
-        r2, rs = _rows_in(residual, d)
-    return d, code, x2, xs, r2, rs, _weight_arg(weight, d)
+        raise ValueError(f"{what} must be [..., d] with d >= 1")
+    return x.shape[-1]
 
 
-def _sum_out(x, residual, s):
-    torch = _torch()
+def _branch(x, residual, s, d: int):
+    """(residual, its stride, s, its stride) of a forward call: the sum is made where there is a residual."""
     if residual is None:
         if s is not None:
             raise ValueError("s is the sum x + residual: pass it with a residual only")
-        return None, 0
+        return None, 0, None, 0
+    if residual.shape != x.shape or residual.dtype != x.dtype:
+        raise ValueError("residual must have x's shape and dtype")
+    residual, rs = _rows_in(residual, d)
     if s is None:
-        s = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    return s, _rows_out(s, x.shape, x.dtype, "s")
+        return residual, rs, _like(x, x.dtype), d
+    return residual, rs, s, _rows_out(s, x.shape, x.dtype, "s")
 
 
 def _codes_out(x, d: int, q, scale):
     """(q [..., d] int8, its row stride, scale [...]); a fresh q has rows on 16-byte boundaries."""
     torch = _torch()
-    lead = tuple(x.shape[:-1])
+    lead = x.shape[:-1]
     if q is None:
-        ld = (d + 15) // 16 * 16
-        q = torch.empty(*lead, ld, dtype=torch.int8, device=x.device)
-        qs = ld
-        if ld != d:
+        qs = (d + 15) // 16 * 16
+        q = x.new_empty((*lead, qs), dtype=torch.int8)
+        if qs != d:
             q = q[..., :d]
     else:
         qs = _rows_out(q, x.shape, torch.int8, "q")
     if scale is None:
-        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
-    elif tuple(scale.shape) != lead or scale.dtype != torch.float32 or not scale.is_contiguous():
-        raise ValueError(f"scale must be a contiguous float32 tensor of shape {lead}")
+        scale = x.new_empty(lead, dtype=torch.float32)
+    elif scale.shape != lead or scale.dtype != torch.float32 or not scale.is_contiguous():
+        raise ValueError(f"scale must be a contiguous float32 tensor of shape {tuple(lead)}")
     return q, qs, scale
 
 
@@ -602,20 +617,22 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, residual=None, out_dtype=None
     in ``out_dtype`` (x's by default), over the last dimension of x [..., d] (fp32 or bf16; weight [d] fp32 or
     bf16, or None for ones).  ``s`` may be x or residual themselves, ``y`` may be x: updated in place."""
     torch = _torch()
-    device = _one_device(x, weight, residual, y, s, dev_status)
-    to = _elsewhere(device, stream)
+    to = _elsewhere(stream, x, weight, residual, y, s, dev_status)
     if to is not None:
         with torch.cuda.stream(to):
             return rms_norm(x, weight, eps=eps, residual=residual, out_dtype=out_dtype, y=y, s=s,
                             dev_status=dev_status)
-    d, code, x2, xs, r2, rs, (wp, wc, _w) = _norm_inputs(x, residual, weight)
-    s, ss = _sum_out(x, residual, s)
+    d, code = _width(x, "x"), _code(x, "x")
+    wp, wc, weight = _weight_arg(weight, d)
+    residual, rs, s, ss = _branch(x, residual, s, d)
     if y is None:
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=device)
-    ys = _rows_out(y, x.shape, out_dtype or y.dtype, "y")
-    rc = lib().rms_norm(_ptr(x2), xs, code, _ptr(r2), rs, wp, wc, x2.shape[0], d, float(eps), _ptr(s), ss, _ptr(y),
-                        ys, _code(y, "y"), _status_word(dev_status), _stream(None))
-    _check("rms_norm", rc)
+        y, ys = _like(x, out_dtype or x.dtype), d
+    else:
+        ys = _rows_out(y, x.shape, out_dtype or y.dtype, "y")
+    x, xs = _rows_in(x, d)
+    _check("rms_norm", lib().rms_norm(
+        x.data_ptr(), xs, code, _ptr(residual), rs, wp, wc, x.numel() // d, d, eps, _ptr(s), ss, y.data_ptr(), ys,
+        _code(y, "y"), _status_word(dev_status), _here(x)))
     return y, s
 
 
@@ -625,17 +642,18 @@ def rms_norm_i8(x, weight=None, *, eps: float = 1e-6, residual=None, q=None, sca
     for y; s as in :func:`rms_norm`.  A fresh q has its rows on 16-byte boundaries (it is a view when d is not a
     multiple of 16), as :func:`matmul_i8` reads them."""
     torch = _torch()
-    device = _one_device(x, weight, residual, q, scale, s, dev_status)
-    to = _elsewhere(device, stream)
+    to = _elsewhere(stream, x, weight, residual, q, scale, s, dev_status)
     if to is not None:
         with torch.cuda.stream(to):
             return rms_norm_i8(x, weight, eps=eps, residual=residual, q=q, scale=scale, s=s, dev_status=dev_status)
-    d, code, x2, xs, r2, rs, (wp, wc, _w) = _norm_inputs(x, residual, weight)
-    s, ss = _sum_out(x, residual, s)
+    d, code = _width(x, "x"), _code(x, "x")
+    wp, wc, weight = _weight_arg(weight, d)
+    residual, rs, s, ss = _branch(x, residual, s, d)
     q, qs, scale = _codes_out(x, d, q, scale)
-    rc = lib().rms_norm_i8(_ptr(x2), xs, code, _ptr(r2), rs, wp, wc, x2.shape[0], d, float(eps), _ptr(s), ss,
-                           _ptr(q), qs, _ptr(scale), _status_word(dev_status), _stream(None))
-    _check("rms_norm_i8", rc)
+    x, xs = _rows_in(x, d)
+    _check("rms_norm_i8", lib().rms_norm_i8(
+        x.data_ptr(), xs, code, _ptr(residual), rs, wp, wc, x.numel() // d, d, eps, _ptr(s), ss, q.data_ptr(), qs,
+        scale.data_ptr(), _status_word(dev_status), _here(x)))
     return q, scale, s
 
 
@@ -643,16 +661,16 @@ def quantize_rows_i8(x, *, q=None, scale=None, dev_status=None, stream=None):
     """(q, scale): the rows of x [..., d] (fp32 or bf16) in int8 with one fp32 scale each, q * scale standing
     for x.  A weight for :func:`matmul_i8` has its output channels as rows: ``quantize_rows_i8(W.t())``."""
     torch = _torch()
-    device = _one_device(x, q, scale, dev_status)
-    to = _elsewhere(device, stream)
+    to = _elsewhere(stream, x, q, scale, dev_status)
     if to is not None:
         with torch.cuda.stream(to):
             return quantize_rows_i8(x, q=q, scale=scale, dev_status=dev_status)
-    d, code, x2, xs, _r, _rs, _wt = _norm_inputs(x, None, None)
+    d, code = _width(x, "x"), _code(x, "x")
     q, qs, scale = _codes_out(x, d, q, scale)
-    rc = lib().quantize_rows_i8(_ptr(x2), xs, code, x2.shape[0], d, _ptr(q), qs, _ptr(scale),
-                                _status_word(dev_status), _stream(None))
-    _check("quantize_rows_i8", rc)
+    x, xs = _rows_in(x, d)
+    _check("quantize_rows_i8", lib().quantize_rows_i8(
+        x.data_ptr(), xs, code, x.numel() // d, d, q.data_ptr(), qs, scale.data_ptr(), _status_word(dev_status),
+        _here(x)))
     return q, scale
 
 
@@ -666,34 +684,39 @@ def rms_norm_backward(dy, s, weight=None, *, eps: float = 1e-6, dsum=None, want_
     itself when there was no residual).  ``dsum`` is the gradient that reaches s from elsewhere; dx (s's dtype) is
     the gradient of x and of the residual alike; dw is fp32 [d], or None when ``want_dw`` is False."""
     torch = _torch()
-    device = _one_device(dy, s, weight, dsum, dx, dw, workspace, dev_status)
-    to = _elsewhere(device, stream)
+    to = _elsewhere(stream, dy, s, weight, dsum, dx, dw, workspace, dev_status)
     if to is not None:
         with torch.cuda.stream(to):
             return rms_norm_backward(dy, s, weight, eps=eps, dsum=dsum, want_dw=want_dw, dx=dx, dw=dw,
                                      workspace=workspace, dev_status=dev_status)
-    d, code, s2, ss, g2, gs, (wp, wc, _w) = _norm_inputs(s, dsum, weight)
+    d, code, dyc = _width(s, "s"), _code(s, "s"), _code(dy, "dy")
     if dy.shape != s.shape:
         raise ValueError("dy must have the shape of s")
-    dyc = _code(dy, "dy")
-    dy2, ys = _rows_in(dy, d)
-    N = s2.shape[0]
+    wp, wc, weight = _weight_arg(weight, d)
+    gs = 0
+    if dsum is not None:
+        if dsum.shape != s.shape or dsum.dtype != s.dtype:
+            raise ValueError("dsum must have the shape and dtype of s")
+        dsum, gs = _rows_in(dsum, d)
     if dx is None:
-        dx = torch.empty(s.shape, dtype=s.dtype, device=device)
-    xs = _rows_out(dx, s.shape, s.dtype, "dx")
+        dx, xs = _like(s, s.dtype), d
+    else:
+        xs = _rows_out(dx, s.shape, s.dtype, "dx")
+    N = s.numel() // d
     ws = None
     if want_dw:
         if dw is None:
-            dw = torch.empty(d, dtype=torch.float32, device=device)
-        elif tuple(dw.shape) != (d,) or dw.dtype != torch.float32 or not dw.is_contiguous():
+            dw = s.new_empty(d, dtype=torch.float32)
+        elif dw.shape != (d,) or dw.dtype != torch.float32 or not dw.is_contiguous():
             raise ValueError(f"dw must be a contiguous float32 tensor of shape ({d},)")
-        ws = _workspace(rms_norm_backward_workspace(N, d), device, workspace)
+        ws = _workspace(rms_norm_backward_workspace(N, d), s.device, workspace)
     elif dw is not None:
         raise ValueError("dw was given with want_dw=False")
-    rc = lib().rms_norm_backward(_ptr(dy2), ys, dyc, _ptr(s2), ss, code, wp, wc, _ptr(g2), gs, N, d, float(eps),
-                                 _ptr(dx), xs, _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel(),
-                                 _status_word(dev_status), _stream(None))
-    _check("rms_norm_backward", rc)
+    dy, ys = _rows_in(dy, d)
+    s, ss = _rows_in(s, d)
+    _check("rms_norm_backward", lib().rms_norm_backward(
+        dy.data_ptr(), ys, dyc, s.data_ptr(), ss, code, wp, wc, _ptr(dsum), gs, N, d, eps, dx.data_ptr(), xs,
+        _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel(), _status_word(dev_status), _here(s)))
     return dx, dw
 
 
@@ -713,10 +736,9 @@ def _operand_i8(t, what: str):
 
 
 def _scales(t, n: int, what: str):
-    torch = _torch()
-    if tuple(t.shape) != (n,) or t.dtype != torch.float32:
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != _torch().float32:
         raise ValueError(f"{what} must be a float32 tensor of shape ({n},)")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def matmul_i8(a, a_scale, b, b_scale, *, bias=None, out_dtype=None, out=None, dev_status=None, stream=None):
@@ -725,30 +747,30 @@ def matmul_i8(a, a_scale, b, b_scale, *, bias=None, out_dtype=None, out=None, de
     Rows that do not start on 16-byte boundaries are copied first; the outputs of :func:`rms_norm_i8` and
     :func:`quantize_rows_i8` do."""
     torch = _torch()
-    device = _one_device(a, a_scale, b, b_scale, bias, out, dev_status)
-    to = _elsewhere(device, stream)
+    to = _elsewhere(stream, a, a_scale, b, b_scale, bias, out, dev_status)
     if to is not None:
         with torch.cuda.stream(to):
             return matmul_i8(a, a_scale, b, b_scale, bias=bias, out_dtype=out_dtype, out=out, dev_status=dev_status)
-    a2, lda = _operand_i8(a, "a")
-    b2, ldb = _operand_i8(b, "b")
-    M, K = a2.shape
-    N = b2.shape[0]
-    if b2.shape[1] != K:
-        raise ValueError(f"a has {K} columns and b {b2.shape[1]}")
+    a, lda = _operand_i8(a, "a")
+    b, ldb = _operand_i8(b, "b")
+    M, K = a.shape
+    N, Kb = b.shape
+    if Kb != K:
+        raise ValueError(f"a has {K} columns and b {Kb}")
     a_scale, b_scale = _scales(a_scale, M, "a_scale"), _scales(b_scale, N, "b_scale")
     bc = DBC_F32
     if bias is not None:
-        if tuple(bias.shape) != (N,):
+        if bias.dim() != 1 or bias.shape[0] != N:
             raise ValueError(f"bias must have shape ({N},)")
         bc = _code(bias, "bias")
         bias = bias.contiguous()
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=device)
-    ldo = _rows_out(out, (M, N), out_dtype or out.dtype, "out")
-    rc = lib().matmul_i8(_ptr(a2), lda, _ptr(a_scale), _ptr(b2), ldb, _ptr(b_scale), _ptr(bias), bc, M, N, K,
-                         _ptr(out), ldo, _code(out, "out"), _status_word(dev_status), _stream(None))
-    _check("matmul_i8", rc)
+        out, ldo = a_scale.new_empty((M, N), dtype=out_dtype or torch.bfloat16), N
+    else:
+        ldo = _rows_out(out, (M, N), out_dtype or out.dtype, "out")
+    _check("matmul_i8", lib().matmul_i8(
+        a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), ldb, b_scale.data_ptr(), _ptr(bias), bc, M, N, K,
+        out.data_ptr(), ldo, _code(out, "out"), _status_word(dev_status), _here(a)))
     return out
 
 
@@ -759,7 +781,7 @@ def chunk_project_i8(H, idx, idx_offsets, weight, W_q, W_scale, *, rows: int, T:
     out = bf16(rms_norm(Z, weight) W) through :func:`rms_norm_i8` and :func:`matmul_i8`.  ``W_q`` int8 [d_g, d]
     and ``W_scale`` fp32 [d_g] come from ``quantize_rows_i8(W_proj.t())``, once."""
     torch = _torch()
-    to = _elsewhere(_one_device(H, idx, idx_offsets, weight, W_q, W_scale, offsets, bias, dev_status), stream)
+    to = _elsewhere(stream, H, idx, idx_offsets, weight, W_q, W_scale, offsets, bias, dev_status)
     if to is not None:
         with torch.cuda.stream(to):
             return chunk_project_i8(H, idx, idx_offsets, weight, W_q, W_scale, rows=rows, T=T, offsets=offsets,
