@@ -249,47 +249,99 @@ struct BwdArgs {
     int32_t *st;
 };
 
-// One row's gradients, given its statistics: dx = rstd (g - xhat c) + ds with
-// c = mean(g xhat), and its terms dy * xhat added to acc.
-template <class TY, class T, int NE, bool DW>
-__device__ __forceinline__ void bwd_frag(const BwdArgs &a, int64_t r, int col, const Frag<TY, NE> &y,
-                                         const Frag<T, NE> &f, const float (&w)[NE], float rstd, float c,
-                                         float (&acc)[NE]) {
-    float o[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const float xh = f.at(i) * rstd;
-        o[i] = rstd * fmaf(-xh, c, y.at(i) * w[i]);
-        if (DW) acc[i] = fmaf(y.at(i), xh, acc[i]);
-    }
-    if (a.ds) {
-        Frag<T, NE> g;
-        g.load(static_cast<const T *>(a.ds) + r * a.ds_s + col);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) o[i] += g.at(i);
-    }
-    Frag<T, NE> q;
-    q.set(o);
-    q.store(static_cast<T *>(a.dx) + r * a.xs + col);
-}
+// Rows on their way to a thread: the fragments of dy, s and ds that it will work on, copied by itself
+// into its own slots of shared memory S rows ahead (cp.async; nobody else reads them, so no barrier).
+// Rows off the 16-byte grid (NE = 1) have no ring and are read when they are due.
+template <class TY, class T, int NE, int NV, int MAXT>
+struct Ring {
+    static constexpr int B = NV * NE * (int)(sizeof(TY) + 2 * sizeof(T));       // a thread's bytes of a row, with ds
+    static constexpr int S = NE == 1 ? 1 : MAXT > 256 ? (B * 2 * MAXT <= 200 * 1024 ? 2 : 1) : B <= 48 ? 4 : B <= 64 ? 3 : 2;
+    static constexpr int kS = NV * NE * (int)sizeof(TY), kDs = kS + NV * NE * (int)sizeof(T);
+    static constexpr int smem(int threads) { return NE == 1 ? 0 : S * B * threads; }
 
-// The same in fp64, for rows whose sums leave fp32's range.
-template <class TY, class T, int NE, bool DW>
-__device__ __noinline__ void bwd_frag_wide(const BwdArgs &a, int64_t r, int col, const Frag<TY, NE> &y,
-                                           const Frag<T, NE> &f, const float (&w)[NE], double rstd, double c,
-                                           float (&acc)[NE]) {
-    Frag<T, NE> g;
-    g.zero();
-    if (a.ds) g.load(static_cast<const T *>(a.ds) + r * a.ds_s + col);
-    float o[NE];
-    for (int i = 0; i < NE; ++i) {
-        const double xh = f.at(i) * rstd, dy = y.at(i);
-        o[i] = (float)(rstd * (dy * w[i] - xh * c) + g.at(i));
-        if (DW) acc[i] += (float)(dy * xh);
+    template <class V>
+    static __device__ __forceinline__ void copy(uint32_t dst, const V *src, bool in, int threads) {
+        constexpr int bytes = NE * (int)sizeof(V);
+        if constexpr (bytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < bytes / 16; ++i)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * threads * 16),
+                             "l"(reinterpret_cast<const char *>(src) + i * 16), "r"(in ? 16 : 0)
+                             : "memory");
+        } else if constexpr (bytes >= 4) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(in ? bytes : 0),
+                         "n"(bytes)
+                         : "memory");
+        }
     }
-    g.set(o);
-    g.store(static_cast<T *>(a.dx) + r * a.xs + col);
-}
+    // Starts the copies of row r (nothing, but still a group, when r is past the end).
+    static __device__ __forceinline__ void start(const BwdArgs &a, uint32_t base, int stage, int64_t r, int t, int W,
+                                                 int threads) {
+        if constexpr (NE > 1) {
+            const uint32_t st = base + stage * B * threads;
+            const bool row = r < a.N;
+            const int64_t rr = row ? r : 0;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (j * W + t) * NE;
+                const bool in = row && col < a.d;
+                const int c = in ? col : 0;
+                constexpr int uy = NE * (int)sizeof(TY) < 16 ? NE * (int)sizeof(TY) : 16;
+                constexpr int us = NE * (int)sizeof(T) < 16 ? NE * (int)sizeof(T) : 16;
+                const int me = threadIdx.x;
+                copy(st + (j * NE * (int)sizeof(TY)) * threads + me * uy, static_cast<const TY *>(a.dy) + rr * a.ys + c, in,
+                     threads);
+                copy(st + (kS + j * NE * (int)sizeof(T)) * threads + me * us, static_cast<const T *>(a.s) + rr * a.ss + c,
+                     in, threads);
+                if (a.ds)
+                    copy(st + (kDs + j * NE * (int)sizeof(T)) * threads + me * us,
+                         static_cast<const T *>(a.ds) + rr * a.ds_s + c, in, threads);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    static __device__ __forceinline__ void wait() {
+        if constexpr (NE > 1) asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    }
+    template <class V>
+    static __device__ __forceinline__ void read(Frag<V, NE> &f, const char *smem, int at, int threads) {
+        constexpr int bytes = NE * (int)sizeof(V), u = bytes < 16 ? bytes : 16;
+        const char *p = smem + at * threads + threadIdx.x * u;
+        uint32_t w[bytes / 4 ? bytes / 4 : 1];
+        if constexpr (u == 16) {
+#pragma unroll
+            for (int i = 0; i < bytes / 16; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(p + i * threads * 16);
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            }
+        } else if constexpr (u == 8) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            w[0] = x.x, w[1] = x.y;
+        }
+        f.from_words(w);
+    }
+    // Fragment j of row r's dy and s; then of its ds.
+    static __device__ __forceinline__ void get(const BwdArgs &a, const char *smem, int stage, int64_t r, int j, int col,
+                                               int threads, Frag<TY, NE> &y, Frag<T, NE> &f) {
+        if constexpr (NE > 1) {
+            const char *st = smem + stage * B * threads;
+            read(y, st, j * NE * (int)sizeof(TY), threads);
+            read(f, st, kS + j * NE * (int)sizeof(T), threads);
+        } else {
+            y.zero();
+            f.zero();
+            if (r < a.N && col < a.d) {
+                y.load(static_cast<const TY *>(a.dy) + r * a.ys + col);
+                f.load(static_cast<const T *>(a.s) + r * a.ss + col);
+            }
+        }
+    }
+    static __device__ __forceinline__ void get_ds(const BwdArgs &a, const char *smem, int stage, int64_t r, int j,
+                                                  int col, int threads, Frag<T, NE> &g) {
+        if constexpr (NE > 1) read(g, smem + stage * B * threads, kDs + j * NE * (int)sizeof(T), threads);
+        else g.load(static_cast<const T *>(a.ds) + r * a.ds_s + col);
+    }
+};
 
 template <class TY, class T, int NE>
 __device__ __forceinline__ void bwd_stats(const Frag<TY, NE> &y, const Frag<T, NE> &f, const float (&w)[NE],
@@ -303,21 +355,60 @@ __device__ __forceinline__ void bwd_stats(const Frag<TY, NE> &y, const Frag<T, N
 template <class TY, class T, int NE>
 __device__ __forceinline__ void bwd_stats_wide(const Frag<TY, NE> &y, const Frag<T, NE> &f, const float (&w)[NE],
                                                double &ss, double &sg) {
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < NE; ++i) {
-        const double v = f.at(i);
-        ss += v * v;
-        sg += (double)y.at(i) * w[i] * v;
+        float v = 0.f, g = 0.f;
+#pragma unroll
+        for (int k = 0; k < NE; ++k)
+            if (k == i) v = f.at(k), g = y.at(k) * w[k];
+        ss += (double)v * v;
+        sg += (double)g * v;
     }
 }
 __device__ __forceinline__ bool in_range(float ss, float sg) { return ss >= kLow && ss <= kHigh && isfinite(sg); }
 
-// Teams of W lanes walk the rows R at a time; a lane keeps the dw sums of its
-// own columns in registers, the CTA joins them at the end (a fixed order).
-template <class TY, class T, int NE, bool DW, int W, int NV, int R>
+// dx = rstd (g - xhat c) + ds with xhat = s rstd and c = mean(g xhat); rstd as in RowFactor.
+struct BwdFactor {
+    RowFactor k;
+    float c;
+    __device__ __forceinline__ BwdFactor(float ss, float sg, int d, float eps) : k(ss, d, eps) {
+        c = sg / (float)d * k.rstd;
+    }
+    __device__ __forceinline__ BwdFactor(double ss, double sg, int d, float eps) : k(ss, d, eps) {
+        c = (float)(sg / d * (double)k.rstd * (double)k.pre);
+    }
+};
+
+template <class Q, bool DW, class TY, class T, int NE>
+__device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int stage, int64_t r, int j, int col,
+                                         int threads, const Frag<TY, NE> &y, const Frag<T, NE> &f,
+                                         const float (&w)[NE], const BwdFactor &k, float (&acc)[NE]) {
+    float o[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const float xh = f.at(i) * k.k.pre * k.k.rstd;
+        o[i] = fmaf(-xh, k.c, y.at(i) * w[i]) * k.k.rstd * k.k.pre;
+        if (DW) acc[i] = fmaf(y.at(i), xh, acc[i]);
+    }
+    Frag<T, NE> q;
+    if (a.ds) {
+        Q::get_ds(a, smem, stage, r, j, col, threads, q);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) o[i] += q.at(i);
+    }
+    q.set(o);
+    q.store(static_cast<T *>(a.dx) + r * a.xs + col);
+}
+
+// Teams of W lanes walk the rows; a lane keeps the dw sums of its own columns
+// in registers, the CTA joins them at the end (a fixed order).
+template <class TY, class T, int NE, bool DW, int W, int NV>
 __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
+    using Q = Ring<TY, T, NE, NV, kThreads>;
+    extern __shared__ __align__(16) char smem[];
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     const int t = threadIdx.x % W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / W) * R;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / W);
     float w[NV][NE], acc[NV][NE];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -326,51 +417,40 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
         for (int i = 0; i < NE; ++i) w[j][i] = 1.f, acc[j][i] = 0.f;
         if (col < a.d) a.w.get<NE>(col, w[j]);
     }
-    // all teams of a warp take the same number of steps: the first team's rows decide
-    const int64_t first = ((int64_t)blockIdx.x * (kThreads / W) + (threadIdx.x & ~31) / W) * R;
+    // all teams of a warp take the same number of steps: the first team's row decides
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / W) + (threadIdx.x & ~31) / W, mine = lane / W;
+    for (int k = 0; k < Q::S - 1; ++k) Q::start(a, base, k, first + k * step + mine, t, W, kThreads);
+    int stage = 0;
     for (int64_t rw = first; rw < a.N; rw += step) {
-        const int64_t r0 = rw + lane / W * R;
-        Frag<TY, NE> y[R][NV];
-        Frag<T, NE> f[R][NV];
+        const int64_t r = rw + mine;
+        Q::start(a, base, stage == 0 ? Q::S - 1 : stage - 1, r + (Q::S - 1) * step, t, W, kThreads);
+        Q::wait();
+        Frag<TY, NE> y[NV];
+        Frag<T, NE> f[NV];
+        float ss = 0.f, sg = 0.f;
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int j = 0; j < NV; ++j) Q::get(a, smem, stage, r, j, (j * W + t) * NE, kThreads, y[j], f[j]);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = (j * W + t) * NE;
-                y[i][j].zero();
-                f[i][j].zero();
-                if (r0 + i < a.N && col < a.d) {
-                    y[i][j].load(static_cast<const TY *>(a.dy) + (r0 + i) * a.ys + col);
-                    f[i][j].load(static_cast<const T *>(a.s) + (r0 + i) * a.ss + col);
-                }
-            }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float ss = 0.f, sg = 0.f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) bwd_stats(y[i][j], f[i][j], w[j], ss, sg);
-            ss = team_reduce<W>(ss, Add());
-            sg = team_reduce<W>(sg, Add());
-            const bool ok = in_range(ss, sg);
+        for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], ss, sg);
+        ss = team_reduce<W>(ss, Add());
+        sg = team_reduce<W>(sg, Add());
+        BwdFactor k(ss, sg, a.d, a.eps);
+        if (__any_sync(0xffffffffu, !in_range(ss, sg))) {
             double s2 = 0, g2 = 0;
-            if (__any_sync(0xffffffffu, !ok)) {
 #pragma unroll
-                for (int j = 0; j < NV; ++j) bwd_stats_wide(y[i][j], f[i][j], w[j], s2, g2);
-                s2 = team_reduce<W>(s2, Add());
-                g2 = team_reduce<W>(g2, Add());
-                if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
-            }
-            const float rstd = rsqrtf(ss / (float)a.d + a.eps), c = sg / (float)a.d * rstd;
-            const double rstd2 = ok ? 0 : 1.0 / sqrt(s2 / a.d + (double)a.eps), c2 = ok ? 0 : g2 / a.d * rstd2;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = (j * W + t) * NE;
-                if (r0 + i < a.N && col < a.d) {
-                    if (ok) bwd_frag<TY, T, NE, DW>(a, r0 + i, col, y[i][j], f[i][j], w[j], rstd, c, acc[j]);
-                    else bwd_frag_wide<TY, T, NE, DW>(a, r0 + i, col, y[i][j], f[i][j], w[j], rstd2, c2, acc[j]);
-                }
-            }
+            for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
+            s2 = team_reduce<W>(s2, Add());
+            g2 = team_reduce<W>(g2, Add());
+            if (!in_range(ss, sg)) k = BwdFactor(s2, g2, a.d, a.eps);   // not the warp's other rows
+            if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
         }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+            if (r < a.N && col < a.d)
+                bwd_frag<Q, DW>(a, smem, stage, r, j, col, kThreads, y[j], f[j], w[j], k, acc[j]);
+        }
+        if (++stage == Q::S) stage = 0;
     }
     if constexpr (DW) {
         __shared__ float sm[kThreads / 32][NV * W * NE];
@@ -394,55 +474,43 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
 }
 
 // Wide rows: one row per CTA at a time, NV fragments per thread.
-template <class TY, class T, int NE, bool DW, int NV>
-__global__ void __launch_bounds__(1024) bwd_block_kernel(const BwdArgs a) {
+template <class TY, class T, int NE, bool DW, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
+    using Q = Ring<TY, T, NE, NV, MAXT>;
+    extern __shared__ __align__(16) char smem[];
     __shared__ float2 part[2][32];
     __shared__ double2 wide[32];
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     const int t = threadIdx.x, W = blockDim.x, lane = t & 31, warp = t >> 5, warps = W >> 5;
-    float acc[NV][NE];
+    float w[NV][NE], acc[NV][NE];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+        const int col = (j * W + t) * NE;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) acc[j][i] = 0.f;
-    int ph = 0;
+        for (int i = 0; i < NE; ++i) w[j][i] = 1.f, acc[j][i] = 0.f;
+        if (col < a.d) a.w.get<NE>(col, w[j]);
+    }
+    for (int k = 0; k < Q::S - 1; ++k) Q::start(a, base, k, blockIdx.x + (int64_t)k * gridDim.x, t, W, W);
+    int ph = 0, stage = 0;
     for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, ph ^= 1) {
+        Q::start(a, base, stage == 0 ? Q::S - 1 : stage - 1, r + (int64_t)(Q::S - 1) * gridDim.x, t, W, W);
+        Q::wait();
         Frag<TY, NE> y[NV];
         Frag<T, NE> f[NV];
-        float w[NV][NE];
         float ss = 0.f, sg = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (j * W + t) * NE;
-            y[j].zero();
-            f[j].zero();
-            if (col < a.d) {
-                y[j].load(static_cast<const TY *>(a.dy) + r * a.ys + col);
-                f[j].load(static_cast<const T *>(a.s) + r * a.ss + col);
-            }
-        }
+        for (int j = 0; j < NV; ++j) Q::get(a, smem, stage, r, j, (j * W + t) * NE, W, y[j], f[j]);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (j * W + t) * NE;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) w[j][i] = 1.f;
-            if (col < a.d) a.w.get<NE>(col, w[j]);
-            bwd_stats(y[j], f[j], w[j], ss, sg);
-        }
+        for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], ss, sg);
         ss = team_reduce<32>(ss, Add());
         sg = team_reduce<32>(sg, Add());
         if (lane == 0) part[ph][warp] = make_float2(ss, sg);
-        __syncthreads();             // the other buffer's readers are past the previous row's barrier
+        __syncthreads();             // the other buffer's readers are past the row before's barrier
         const float2 v = lane < warps ? part[ph][lane] : make_float2(0.f, 0.f);
         ss = team_reduce<32>(v.x, Add());
         sg = team_reduce<32>(v.y, Add());
-        if (in_range(ss, sg)) {      // the same in every thread
-            const float rstd = rsqrtf(ss / (float)a.d + a.eps), c = sg / (float)a.d * rstd;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = (j * W + t) * NE;
-                if (col < a.d) bwd_frag<TY, T, NE, DW>(a, r, col, y[j], f[j], w[j], rstd, c, acc[j]);
-            }
-        } else {
+        BwdFactor k(ss, sg, a.d, a.eps);
+        if (!in_range(ss, sg)) {     // the same in every thread
             double s2 = 0, g2 = 0;
 #pragma unroll
             for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
@@ -453,14 +521,15 @@ __global__ void __launch_bounds__(1024) bwd_block_kernel(const BwdArgs a) {
             const double2 v2 = lane < warps ? wide[lane] : make_double2(0, 0);
             s2 = team_reduce<32>(v2.x, Add());
             g2 = team_reduce<32>(v2.y, Add());
+            k = BwdFactor(s2, g2, a.d, a.eps);
             if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
-            const double rstd = 1.0 / sqrt(s2 / a.d + (double)a.eps), c = g2 / a.d * rstd;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = (j * W + t) * NE;
-                if (col < a.d) bwd_frag_wide<TY, T, NE, DW>(a, r, col, y[j], f[j], w[j], rstd, c, acc[j]);
-            }
         }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+            if (col < a.d) bwd_frag<Q, DW>(a, smem, stage, r, j, col, W, y[j], f[j], w[j], k, acc[j]);
+        }
+        if (++stage == Q::S) stage = 0;
     }
     if constexpr (DW) {
 #pragma unroll
@@ -473,20 +542,26 @@ __global__ void __launch_bounds__(1024) bwd_block_kernel(const BwdArgs a) {
     }
 }
 
-// dw = the CTAs' lines added up, in a fixed order: 32 columns per CTA, 32
-// threads per column.
+// dw = the CTAs' lines added up, in a fixed order: 8 columns (one 32-byte
+// sector of every line) per CTA, 128 threads per column.
 __global__ void __launch_bounds__(1024) dw_kernel(const float *part, int lines, int d, float *dw) {
-    __shared__ double sm[32][33];
-    const int c = threadIdx.x & 31, k = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+    __shared__ double sm[32][8];
+    const int c = threadIdx.x & 7, k = threadIdx.x >> 3, col = blockIdx.x * 8 + c;
+    float v[10];                                     // lines <= 148 * 8 < 128 * 10
+#pragma unroll
+    for (int i = 0; i < 10; ++i) v[i] = col < d && k + i * 128 < lines ? part[(int64_t)(k + i * 128) * d + col] : 0.f;
     double t = 0;
-    if (col < d) {
-#pragma unroll 8
-        for (int r = k; r < lines; r += 32) t += part[(int64_t)r * d + col];
-    }
-    sm[k][c] = t;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) t += v[i];
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
+    if ((threadIdx.x & 31) < 8) sm[threadIdx.x >> 5][c] = t;
     __syncthreads();
-    t = team_reduce<32>(sm[c][k], Add());
-    if (c == 0 && blockIdx.x * 32 + k < d) dw[blockIdx.x * 32 + k] = (float)t;
+    if (threadIdx.x < 256) {                         // warp w: column w
+        t = team_reduce<32>(sm[threadIdx.x & 31][threadIdx.x >> 5], Add());
+        const int out = blockIdx.x * 8 + (threadIdx.x >> 5);
+        if ((threadIdx.x & 31) == 0 && out < d) dw[out] = (float)t;
+    }
 }
 
 inline bool aligned_to(const void *p, int64_t e) { return (reinterpret_cast<uintptr_t>(p) % e) == 0; }
@@ -583,43 +658,63 @@ dbc_status launch_fwd(const FwdArgs &a, int dtype, cudaStream_t st) {
     return launch_status();
 }
 
-// CTAs of a backward call, and with them the lines of dw sums: up to 8 per SM,
-// fewer for wide rows, whose lines would otherwise outweigh the rows.
-inline int bwd_ctas(int64_t N, int64_t d) {
-    return (int)std::min<int64_t>(N, 148 * std::min<int64_t>(8, std::max<int64_t>(1, kMaxD / d)));
+// The most CTAs of a backward call, and with them the lines of dw sums: up to
+// 8 per SM, fewer for wide rows, whose lines would otherwise outweigh the rows.
+constexpr int kSms = 148;
+inline int bwd_lines(int64_t N, int64_t d) {
+    return (int)std::min<int64_t>(N, kSms * std::min<int64_t>(8, std::max<int64_t>(1, kMaxD / d)));
 }
 
-template <class TY, class T, int NE, int W, int NV, int R>
-void launch_bwd_team(const BwdArgs &a, int ctas, cudaStream_t st) {
-    if (a.part) bwd_team_kernel<TY, T, NE, true, W, NV, R><<<ctas, kThreads, 0, st>>>(a);
-    else bwd_team_kernel<TY, T, NE, false, W, NV, R><<<ctas, kThreads, 0, st>>>(a);
+// Launches as many CTAs as are resident at once, at most `most`; returns them
+// (0: a CUDA error).
+template <class K>
+int launch_resident(K kernel, const BwdArgs &a, int threads, int smem, int64_t most, cudaStream_t st) {
+    int per_sm = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+        return 0;
+    const int ctas = (int)std::min<int64_t>(most, (int64_t)per_sm * kSms);
+    kernel<<<ctas, threads, smem, st>>>(a);
+    return ctas;
 }
 
-template <class TY, class T, int NE, int NV>
-void launch_bwd_block(const BwdArgs &a, int ctas, cudaStream_t st) {
+template <class TY, class T, int NE, int W, int NV>
+int launch_bwd_team(const BwdArgs &a, cudaStream_t st) {
+    const int smem = Ring<TY, T, NE, NV, kThreads>::smem(kThreads);
+    constexpr int rows = kThreads / W;
+    const int64_t most = std::min<int64_t>(bwd_lines(a.N, a.d), (a.N + rows - 1) / rows);
+    return a.part ? launch_resident(bwd_team_kernel<TY, T, NE, true, W, NV>, a, kThreads, smem, most, st)
+                  : launch_resident(bwd_team_kernel<TY, T, NE, false, W, NV>, a, kThreads, smem, most, st);
+}
+
+template <class TY, class T, int NE, int NV, int MAXT>
+int launch_bwd_block(const BwdArgs &a, cudaStream_t st) {
     const int threads = ((a.d + NE * NV - 1) / (NE * NV) + 31) / 32 * 32;
-    if (a.part) bwd_block_kernel<TY, T, NE, true, NV><<<ctas, threads, 0, st>>>(a);
-    else bwd_block_kernel<TY, T, NE, false, NV><<<ctas, threads, 0, st>>>(a);
+    const int smem = Ring<TY, T, NE, NV, MAXT>::smem(threads), most = bwd_lines(a.N, a.d);
+    return a.part ? launch_resident(bwd_block_kernel<TY, T, NE, true, NV, MAXT>, a, threads, smem, most, st)
+                  : launch_resident(bwd_block_kernel<TY, T, NE, false, NV, MAXT>, a, threads, smem, most, st);
 }
 
 template <class TY, class T>
-void launch_bwd(const BwdArgs &a, int ctas, cudaStream_t st) {
+int launch_bwd(const BwdArgs &a, cudaStream_t st) {
     constexpr int E = 16 / sizeof(T);
     const int64_t e = sizeof(T), ey = sizeof(TY);
     const bool vec = a.d % E == 0 && on_grid(a.s, a.ss, e, 16) && on_grid(a.ds, a.ds_s, e, 16) &&
                      on_grid(a.dx, a.xs, e, 16) && on_grid(a.dy, a.ys, ey, std::min<int64_t>(16, E * ey)) &&
                      on_grid(a.w.p, 0, 1, a.w.bf16 ? E * 2 : 16);
     if (!vec) {
-        if (a.d <= 256) return launch_bwd_team<TY, T, 1, 32, 8, 1>(a, ctas, st);
-        return launch_bwd_block<TY, T, 1, 16>(a, ctas, st);
+        if (a.d <= 256) return launch_bwd_team<TY, T, 1, 32, 8>(a, st);
+        if (a.d <= 2048) return launch_bwd_block<TY, T, 1, 8, 256>(a, st);
+        return launch_bwd_block<TY, T, 1, 16, 1024>(a, st);
     }
     const int V = a.d / E;
-    if (V <= 8) return launch_bwd_team<TY, T, E, 8, 1, 2>(a, ctas, st);
-    if (V <= 16) return launch_bwd_team<TY, T, E, 16, 1, 2>(a, ctas, st);
-    if (V <= 32) return launch_bwd_team<TY, T, E, 32, 1, 2>(a, ctas, st);
-    if (V <= 64) return launch_bwd_team<TY, T, E, 32, 2, 1>(a, ctas, st);
-    if (V <= 2048) return launch_bwd_block<TY, T, E, 2>(a, ctas, st);
-    return launch_bwd_block<TY, T, E, 4>(a, ctas, st);
+    if (V <= 8) return launch_bwd_team<TY, T, E, 8, 1>(a, st);
+    if (V <= 16) return launch_bwd_team<TY, T, E, 16, 1>(a, st);
+    if (V <= 32) return launch_bwd_team<TY, T, E, 32, 1>(a, st);
+    if (V <= 64) return launch_bwd_team<TY, T, E, 32, 2>(a, st);
+    if (V <= 512) return launch_bwd_block<TY, T, E, 2, 256>(a, st);
+    if (V <= 2048) return launch_bwd_block<TY, T, E, 2, 1024>(a, st);
+    return launch_bwd_block<TY, T, E, 4, 1024>(a, st);
 }
 
 }  // namespace nm
@@ -673,7 +768,7 @@ extern "C" dbc_status quantize_rows_i8(const void *x, int64_t x_stride, int dtyp
 
 extern "C" size_t rms_norm_backward_workspace(int64_t N, int64_t d) {
     if (N <= 0 || d <= 0) return 0;
-    return align_up((size_t)nm::bwd_ctas(N, d) * (size_t)d * sizeof(float));
+    return align_up((size_t)nm::bwd_lines(N, d) * (size_t)d * sizeof(float));
 }
 
 extern "C" dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int dy_dtype, const void *s,
@@ -698,15 +793,16 @@ extern "C" dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int d
     }
     if (dw && (!ws || !nm::aligned_to(ws, 16) || ws_bytes < rms_norm_backward_workspace(N, d)))
         return DBC_ERR_WORKSPACE;
-    const int ctas = nm::bwd_ctas(N, d);
     const nm::BwdArgs a{dy, s, ds, dx, {weight, w_dtype == DBC_BF16}, dy_stride, s_stride, ds_stride, dx_stride, N,
                         (int)d, eps, dw ? static_cast<float *>(ws) : nullptr, dev_status};
     using B = __nv_bfloat16;
-    if (dy_dtype == DBC_BF16 && dtype == DBC_BF16) nm::launch_bwd<B, B>(a, ctas, st);
-    else if (dy_dtype == DBC_BF16) nm::launch_bwd<B, float>(a, ctas, st);
-    else if (dtype == DBC_BF16) nm::launch_bwd<float, B>(a, ctas, st);
-    else nm::launch_bwd<float, float>(a, ctas, st);
-    if (dw) nm::dw_kernel<<<(unsigned)((d + 31) / 32), 1024, 0, st>>>(static_cast<const float *>(ws), ctas, (int)d, dw);
+    const bool by = dy_dtype == DBC_BF16, bs = dtype == DBC_BF16;
+    const int lines = by && bs ? nm::launch_bwd<B, B>(a, st)
+                      : by     ? nm::launch_bwd<B, float>(a, st)
+                      : bs     ? nm::launch_bwd<float, B>(a, st)
+                               : nm::launch_bwd<float, float>(a, st);
+    if (!lines) return DBC_ERR_CUDA;
+    if (dw) nm::dw_kernel<<<(unsigned)((d + 7) / 8), 1024, 0, st>>>(a.part, lines, (int)d, dw);
     count_launches(dw ? 2 : 1);
     return launch_status();
 }

@@ -28,6 +28,10 @@ struct Frag<__nv_bfloat16, 8> {
     __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
         *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    __device__ __forceinline__ void from_words(const uint32_t (&u)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = u[i];
+    }
     __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
     __device__ __forceinline__ float at(int i) const {
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
@@ -55,6 +59,7 @@ struct Frag<__nv_bfloat16, 4> {
     __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
         *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
+    __device__ __forceinline__ void from_words(const uint32_t (&u)[2]) { w[0] = u[0], w[1] = u[1]; }
     __device__ __forceinline__ void zero() { w[0] = w[1] = 0; }
     __device__ __forceinline__ float at(int i) const {
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
@@ -118,6 +123,10 @@ struct Frag<float, NE> {
             for (int i = 0; i < NE / 4; ++i)
                 reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
+    }
+    __device__ __forceinline__ void from_words(const uint32_t (&u)[NE]) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] = __uint_as_float(u[i]);
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
