@@ -11,47 +11,10 @@
 // team of 8, 16 or 32 lanes, R rows at a time so that each thread keeps about
 // four loads per input in flight; wider rows belong to a CTA.
 #include "norm.cuh"
+#include "norm_odd.cuh"
 
 namespace dbc {
 namespace nm {
-
-constexpr int kThreads = 256;
-constexpr int64_t kMaxD = 16384;
-constexpr float kLow = 1e-30f, kHigh = 1e37f;
-
-// kI8Narrow: the norm's 8-bit form where s * w has 16 significant bits (bf16
-// rows, bf16 weight or none); kQuant: no norm, p = x.
-enum { kPlain = 0, kI8 = 1, kI8Narrow = 2, kQuant = 3 };
-constexpr bool norms(int mode) { return mode != kQuant; }
-constexpr bool weighs(int mode) { return mode == kI8 || mode == kI8Narrow; }
-template <class T>
-constexpr bool narrow(int mode) { return mode == kI8Narrow || (mode == kQuant && sizeof(T) == 2); }
-
-struct FwdArgs {
-    const void *x, *res;
-    void *s, *y;
-    int8_t *q;
-    float *scale;
-    Weight w;
-    int64_t xs, rs, ss, ys, qs, N;
-    int d, y_bf16;
-    float eps;
-    int32_t *st;
-};
-
-// What the row's statistics say: the factors of y = (s * pre) * rstd * w (pre
-// is 1 unless rstd would be subnormal) and the 8-bit scale.
-struct RowFactor {
-    float pre, rstd;
-    __device__ __forceinline__ RowFactor(float ss, int d, float eps) : pre(1.f) {
-        rstd = rsqrtf(ss / (float)d + eps);
-    }
-    __device__ __forceinline__ RowFactor(double ss, int d, float eps) {
-        const double r = 1.0 / sqrt(ss / d + (double)eps);
-        pre = r < 0x1p-120 ? 0x1p-16f : 1.f;
-        rstd = (float)(r / (double)pre);
-    }
-};
 
 // One row from registers to memory (s, then y or q), fragment column `col`.
 template <class T, int NE, int MODE, bool RES>
@@ -69,15 +32,6 @@ __device__ __forceinline__ void write_frag(const FwdArgs &a, int64_t r, int col,
         for (int i = 0; i < NE; ++i) p[i] = weighs(MODE) ? f.at(i) * w[i] : f.at(i);
         qn.template store<narrow<T>(MODE), NE>(a.q + r * a.qs + col, p);
     }
-}
-
-template <int MODE>
-__device__ __forceinline__ float row_scale(const Quant &q, const RowFactor &k) {
-    if (q.bad) return __int_as_float(0x7fc00000);
-    const float m = q.m;
-    if (!norms(MODE)) return m / 127.f;
-    // the order that leaves fp32's normal range only where the scale itself does
-    return m < 1.f ? m * k.rstd * k.pre / 127.f : m / 127.f * k.pre * k.rstd;
 }
 
 template <class T, int NE>
@@ -238,26 +192,14 @@ __global__ void __launch_bounds__(1024) block_kernel(const FwdArgs a) {
     }
 }
 
-struct BwdArgs {
-    const void *dy, *s, *ds;
-    void *dx;
-    Weight w;
-    int64_t ys, ss, ds_s, xs, N;
-    int d;
-    float eps;
-    float *part;                 // one line of d dw sums per CTA, or NULL
-    int32_t *st;
-};
-
 // Rows on their way to a thread: the fragments of dy, s and ds that it will work on, copied by itself
 // into its own slots of shared memory S rows ahead (cp.async; nobody else reads them, so no barrier).
-// Rows off the 16-byte grid (NE = 1) have no ring and are read when they are due.
 template <class TY, class T, int NE, int NV, int MAXT>
 struct Ring {
     static constexpr int B = NV * NE * (int)(sizeof(TY) + 2 * sizeof(T));       // a thread's bytes of a row, with ds
-    static constexpr int S = NE == 1 ? 1 : MAXT > 256 ? (B * 2 * MAXT <= 200 * 1024 ? 2 : 1) : B <= 48 ? 4 : B <= 64 ? 3 : 2;
+    static constexpr int S = MAXT > 256 ? (B * 2 * MAXT <= 200 * 1024 ? 2 : 1) : B <= 48 ? 4 : B <= 64 ? 3 : 2;
     static constexpr int kS = NV * NE * (int)sizeof(TY), kDs = kS + NV * NE * (int)sizeof(T);
-    static constexpr int smem(int threads) { return NE == 1 ? 0 : S * B * threads; }
+    static constexpr int smem(int threads) { return S * B * threads; }
 
     template <class V>
     static __device__ __forceinline__ void copy(uint32_t dst, const V *src, bool in, int threads) {
@@ -268,7 +210,7 @@ struct Ring {
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * threads * 16),
                              "l"(reinterpret_cast<const char *>(src) + i * 16), "r"(in ? 16 : 0)
                              : "memory");
-        } else if constexpr (bytes >= 4) {
+        } else {
             asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(in ? bytes : 0),
                          "n"(bytes)
                          : "memory");
@@ -277,7 +219,7 @@ struct Ring {
     // Starts the copies of row r (nothing, but still a group, when r is past the end).
     static __device__ __forceinline__ void start(const BwdArgs &a, uint32_t base, int stage, int64_t r, int t, int W,
                                                  int threads) {
-        if constexpr (NE > 1) {
+        {
             const uint32_t st = base + stage * B * threads;
             const bool row = r < a.N;
             const int64_t rr = row ? r : 0;
@@ -301,7 +243,7 @@ struct Ring {
         }
     }
     static __device__ __forceinline__ void wait() {
-        if constexpr (NE > 1) asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
     }
     template <class V>
     static __device__ __forceinline__ void read(Frag<V, NE> &f, const char *smem, int at, int threads) {
@@ -321,25 +263,13 @@ struct Ring {
         f.from_words(w);
     }
     // Fragment j of row r's dy and s; then of its ds.
-    static __device__ __forceinline__ void get(const BwdArgs &a, const char *smem, int stage, int64_t r, int j, int col,
-                                               int threads, Frag<TY, NE> &y, Frag<T, NE> &f) {
-        if constexpr (NE > 1) {
-            const char *st = smem + stage * B * threads;
-            read(y, st, j * NE * (int)sizeof(TY), threads);
-            read(f, st, kS + j * NE * (int)sizeof(T), threads);
-        } else {
-            y.zero();
-            f.zero();
-            if (r < a.N && col < a.d) {
-                y.load(static_cast<const TY *>(a.dy) + r * a.ys + col);
-                f.load(static_cast<const T *>(a.s) + r * a.ss + col);
-            }
-        }
+    static __device__ __forceinline__ void get(const char *smem, int stage, int j, int threads, Frag<TY, NE> &y, Frag<T, NE> &f) {
+        const char *st = smem + stage * B * threads;
+        read(y, st, j * NE * (int)sizeof(TY), threads);
+        read(f, st, kS + j * NE * (int)sizeof(T), threads);
     }
-    static __device__ __forceinline__ void get_ds(const BwdArgs &a, const char *smem, int stage, int64_t r, int j,
-                                                  int col, int threads, Frag<T, NE> &g) {
-        if constexpr (NE > 1) read(g, smem + stage * B * threads, kDs + j * NE * (int)sizeof(T), threads);
-        else g.load(static_cast<const T *>(a.ds) + r * a.ds_s + col);
+    static __device__ __forceinline__ void get_ds(const char *smem, int stage, int j, int threads, Frag<T, NE> &g) {
+        read(g, smem + stage * B * threads, kDs + j * NE * (int)sizeof(T), threads);
     }
 };
 
@@ -365,20 +295,6 @@ __device__ __forceinline__ void bwd_stats_wide(const Frag<TY, NE> &y, const Frag
         sg += (double)g * v;
     }
 }
-__device__ __forceinline__ bool in_range(float ss, float sg) { return ss >= kLow && ss <= kHigh && isfinite(sg); }
-
-// dx = rstd (g - xhat c) + ds with xhat = s rstd and c = mean(g xhat); rstd as in RowFactor.
-struct BwdFactor {
-    RowFactor k;
-    float c;
-    __device__ __forceinline__ BwdFactor(float ss, float sg, int d, float eps) : k(ss, d, eps) {
-        c = sg / (float)d * k.rstd;
-    }
-    __device__ __forceinline__ BwdFactor(double ss, double sg, int d, float eps) : k(ss, d, eps) {
-        c = (float)(sg / d * (double)k.rstd * (double)k.pre);
-    }
-};
-
 template <class Q, bool DW, class TY, class T, int NE>
 __device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int stage, int64_t r, int j, int col,
                                          int threads, const Frag<TY, NE> &y, const Frag<T, NE> &f,
@@ -392,7 +308,7 @@ __device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int
     }
     Frag<T, NE> q;
     if (a.ds) {
-        Q::get_ds(a, smem, stage, r, j, col, threads, q);
+        Q::get_ds(smem, stage, j, threads, q);
 #pragma unroll
         for (int i = 0; i < NE; ++i) o[i] += q.at(i);
     }
@@ -429,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
         Frag<T, NE> f[NV];
         float ss = 0.f, sg = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) Q::get(a, smem, stage, r, j, (j * W + t) * NE, kThreads, y[j], f[j]);
+        for (int j = 0; j < NV; ++j) Q::get(smem, stage, j, kThreads, y[j], f[j]);
 #pragma unroll
         for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], ss, sg);
         ss = team_reduce<W>(ss, Add());
@@ -499,7 +415,7 @@ __global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
         Frag<T, NE> f[NV];
         float ss = 0.f, sg = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) Q::get(a, smem, stage, r, j, (j * W + t) * NE, W, y[j], f[j]);
+        for (int j = 0; j < NV; ++j) Q::get(smem, stage, j, W, y[j], f[j]);
 #pragma unroll
         for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], ss, sg);
         ss = team_reduce<32>(ss, Add());
@@ -617,6 +533,51 @@ dbc_status launch_block(const FwdArgs &a, cudaStream_t st) {
     return DBC_OK;
 }
 
+// As many CTAs as are resident at once, at most `most`; 0 after a CUDA error.
+constexpr int kSms = 148;
+template <class K>
+int resident(K kernel, int threads, int smem, int64_t most) {
+    int per_sm = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+        return 0;
+    return (int)std::min<int64_t>(most, (int64_t)per_sm * kSms);
+}
+
+// Shared memory of one team: two rows ahead of the arithmetic where that leaves
+// room for a second CTA, else one.
+struct OddPlan {
+    int threads, teams, stages, team_bytes, smem;
+};
+inline OddPlan odd_plan(int64_t N, int d, int nv, bool block, int in_bytes, int out_bytes) {
+    OddPlan p;
+    p.threads = block ? ((d + nv - 1) / nv + 31) / 32 * 32 : kThreads;
+    p.teams = block ? 1 : kThreads / 32;
+    p.stages = (2 * in_bytes + out_bytes) * p.teams <= 100 * 1024 ? 2 : 1;
+    p.team_bytes = p.stages * in_bytes + out_bytes;
+    p.smem = p.team_bytes * p.teams;
+    return p;
+}
+
+template <class T, int MODE, bool RES, int NV, bool BLOCK, int MAXT>
+dbc_status launch_odd_res(const FwdArgs &a, cudaStream_t st) {
+    const int slot = slot_bytes(a.d, sizeof(T));
+    const OddPlan p = odd_plan(a.N, a.d, NV, BLOCK, (RES ? 2 : 1) * slot,
+                               slot_bytes(a.d, MODE != kPlain ? 1 : a.y_bf16 ? 2 : 4));
+    auto *k = odd_kernel<T, MODE, RES, NV, BLOCK, MAXT>;
+    const int ctas = resident(k, p.threads, p.smem, (a.N + p.teams - 1) / p.teams);
+    if (!ctas) return DBC_ERR_CUDA;
+    k<<<ctas, p.threads, p.smem, st>>>(a, slot, p.stages, p.team_bytes);
+    return DBC_OK;
+}
+template <class T, int MODE, int NV, bool BLOCK, int MAXT>
+dbc_status launch_odd(const FwdArgs &a, cudaStream_t st) {
+    if constexpr (norms(MODE)) {
+        if (a.res) return launch_odd_res<T, MODE, true, NV, BLOCK, MAXT>(a, st);
+    }
+    return launch_odd_res<T, MODE, false, NV, BLOCK, MAXT>(a, st);
+}
+
 // Several rows per team pay once every SM has work without them.
 inline bool many(int64_t rows, int lanes, int R) { return rows * lanes / 32 / R >= 148 * 16; }
 
@@ -628,9 +589,10 @@ dbc_status launch_rows(const FwdArgs &a, cudaStream_t st) {
                      on_grid(a.s, a.ss, e, 16) && on_grid(a.y, a.ys, ysz, std::min<int64_t>(16, E * ysz)) &&
                      on_grid(a.q, a.qs, 1, E) && on_grid(a.w.p, 0, 1, a.w.bf16 ? E * 2 : 16);
     if (!vec) {
-        if (a.d <= 256) return launch_team<T, 1, MODE, 32, 8, 1>(a, st);
-        if (a.d <= 512) return launch_team<T, 1, MODE, 32, 16, 1>(a, st);
-        return launch_block<T, 1, MODE, 16>(a, st);
+        if (a.d <= 256) return launch_odd<T, MODE, 8, false, kThreads>(a, st);
+        if (a.d <= 512) return launch_odd<T, MODE, 16, false, kThreads>(a, st);
+        if (a.d <= 2048) return launch_odd<T, MODE, 8, true, 256>(a, st);
+        return launch_odd<T, MODE, 16, true, 1024>(a, st);
     }
     const int V = a.d / E;
     if (V <= 8)
@@ -660,21 +622,26 @@ dbc_status launch_fwd(const FwdArgs &a, int dtype, cudaStream_t st) {
 
 // The most CTAs of a backward call, and with them the lines of dw sums: up to
 // 8 per SM, fewer for wide rows, whose lines would otherwise outweigh the rows.
-constexpr int kSms = 148;
 inline int bwd_lines(int64_t N, int64_t d) {
     return (int)std::min<int64_t>(N, kSms * std::min<int64_t>(8, std::max<int64_t>(1, kMaxD / d)));
 }
 
-// Launches as many CTAs as are resident at once, at most `most`; returns them
-// (0: a CUDA error).
 template <class K>
 int launch_resident(K kernel, const BwdArgs &a, int threads, int smem, int64_t most, cudaStream_t st) {
-    int per_sm = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
-        return 0;
-    const int ctas = (int)std::min<int64_t>(most, (int64_t)per_sm * kSms);
-    kernel<<<ctas, threads, smem, st>>>(a);
+    const int ctas = resident(kernel, threads, smem, most);
+    if (ctas) kernel<<<ctas, threads, smem, st>>>(a);
+    return ctas;
+}
+
+template <class TY, class T, int NV, bool BLOCK, int MAXT>
+int launch_odd_bwd(const BwdArgs &a, cudaStream_t st) {
+    const int yslot = slot_bytes(a.d, sizeof(TY)), slot = slot_bytes(a.d, sizeof(T));
+    OddPlan p = odd_plan(a.N, a.d, NV, BLOCK, yslot + (a.ds ? 2 : 1) * slot, 0);
+    if (!BLOCK) p.smem = std::max(p.smem, kThreads / 32 * a.d * 4);       // the warps' lines of dw sums
+    const int64_t most = std::min<int64_t>(bwd_lines(a.N, a.d), (a.N + p.teams - 1) / p.teams);
+    auto *k = a.part ? odd_bwd_kernel<TY, T, true, NV, BLOCK, MAXT> : odd_bwd_kernel<TY, T, false, NV, BLOCK, MAXT>;
+    const int ctas = resident(k, p.threads, p.smem, most);
+    if (ctas) k<<<ctas, p.threads, p.smem, st>>>(a, yslot, slot, p.stages, p.team_bytes);
     return ctas;
 }
 
@@ -703,9 +670,9 @@ int launch_bwd(const BwdArgs &a, cudaStream_t st) {
                      on_grid(a.dx, a.xs, e, 16) && on_grid(a.dy, a.ys, ey, std::min<int64_t>(16, E * ey)) &&
                      on_grid(a.w.p, 0, 1, a.w.bf16 ? E * 2 : 16);
     if (!vec) {
-        if (a.d <= 256) return launch_bwd_team<TY, T, 1, 32, 8>(a, st);
-        if (a.d <= 2048) return launch_bwd_block<TY, T, 1, 8, 256>(a, st);
-        return launch_bwd_block<TY, T, 1, 16, 1024>(a, st);
+        if (a.d <= 256) return launch_odd_bwd<TY, T, 8, false, kThreads>(a, st);
+        if (a.d <= 2048) return launch_odd_bwd<TY, T, 8, true, 256>(a, st);
+        return launch_odd_bwd<TY, T, 16, true, 1024>(a, st);
     }
     const int V = a.d / E;
     if (V <= 8) return launch_bwd_team<TY, T, E, 8, 1>(a, st);

@@ -281,5 +281,85 @@ __device__ __forceinline__ V team_reduce(V v, F f) {
     return v;
 }
 
+// ---------------------------------------------------------------- what the kernels share
+template <class T>
+__device__ __forceinline__ float round_to(float v);
+template <>
+__device__ __forceinline__ float round_to<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float round_to<__nv_bfloat16>(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxD = 16384;
+constexpr float kLow = 1e-30f, kHigh = 1e37f;
+
+// kI8Narrow: the norm's 8-bit form where s * w has 16 significant bits (bf16
+// rows, bf16 weight or none); kQuant: no norm, p = x.
+enum { kPlain = 0, kI8 = 1, kI8Narrow = 2, kQuant = 3 };
+constexpr bool norms(int mode) { return mode != kQuant; }
+constexpr bool weighs(int mode) { return mode == kI8 || mode == kI8Narrow; }
+template <class T>
+constexpr bool narrow(int mode) { return mode == kI8Narrow || (mode == kQuant && sizeof(T) == 2); }
+
+struct FwdArgs {
+    const void *x, *res;
+    void *s, *y;
+    int8_t *q;
+    float *scale;
+    Weight w;
+    int64_t xs, rs, ss, ys, qs, N;
+    int d, y_bf16;
+    float eps;
+    int32_t *st;
+};
+
+// What the row's statistics say: the factors of y = (s * pre) * rstd * w (pre
+// is 1 unless rstd would be subnormal) and the 8-bit scale.
+struct RowFactor {
+    float pre, rstd;
+    __device__ __forceinline__ RowFactor(float ss, int d, float eps) : pre(1.f) {
+        rstd = rsqrtf(ss / (float)d + eps);
+    }
+    __device__ __forceinline__ RowFactor(double ss, int d, float eps) {
+        const double r = 1.0 / sqrt(ss / d + (double)eps);
+        pre = r < 0x1p-120 ? 0x1p-16f : 1.f;
+        rstd = (float)(r / (double)pre);
+    }
+};
+
+template <int MODE>
+__device__ __forceinline__ float row_scale(const Quant &q, const RowFactor &k) {
+    if (q.bad) return __int_as_float(0x7fc00000);
+    const float m = q.m;
+    if (!norms(MODE)) return m / 127.f;
+    // the order that leaves fp32's normal range only where the scale itself does
+    return m < 1.f ? m * k.rstd * k.pre / 127.f : m / 127.f * k.pre * k.rstd;
+}
+
+struct BwdArgs {
+    const void *dy, *s, *ds;
+    void *dx;
+    Weight w;
+    int64_t ys, ss, ds_s, xs, N;
+    int d;
+    float eps;
+    float *part;                 // one line of d dw sums per CTA, or NULL
+    int32_t *st;
+};
+
+__device__ __forceinline__ bool in_range(float ss, float sg) { return ss >= kLow && ss <= kHigh && isfinite(sg); }
+
+// dx = rstd (g - xhat c) + ds with xhat = s rstd and c = mean(g xhat); rstd as in RowFactor.
+struct BwdFactor {
+    RowFactor k;
+    float c;
+    __device__ __forceinline__ BwdFactor(float ss, float sg, int d, float eps) : k(ss, d, eps) {
+        c = sg / (float)d * k.rstd;
+    }
+    __device__ __forceinline__ BwdFactor(double ss, double sg, int d, float eps) : k(ss, d, eps) {
+        c = (float)(sg / d * (double)k.rstd * (double)k.pre);
+    }
+};
+
 }  // namespace nm
 }  // namespace dbc
