@@ -544,38 +544,58 @@ int resident(K kernel, int threads, int smem, int64_t most) {
     return (int)std::min<int64_t>(most, (int64_t)per_sm * kSms);
 }
 
-// Shared memory of one team: two rows ahead of the arithmetic where that leaves
-// room for a second CTA, else one.
+// Threads, rows in shared memory (two where that leaves room for a second CTA)
+// and bytes of the kernels that give a row to a CTA.
 struct OddPlan {
-    int threads, teams, stages, team_bytes, smem;
+    int threads, stages, smem;
 };
-inline OddPlan odd_plan(int64_t N, int d, int nv, bool block, int in_bytes, int out_bytes) {
-    OddPlan p;
-    p.threads = block ? ((d + nv - 1) / nv + 31) / 32 * 32 : kThreads;
-    p.teams = block ? 1 : kThreads / 32;
-    p.stages = (2 * in_bytes + out_bytes) * p.teams <= 100 * 1024 ? 2 : 1;
-    p.team_bytes = p.stages * in_bytes + out_bytes;
-    p.smem = p.team_bytes * p.teams;
-    return p;
+inline OddPlan odd_plan(int d, int nv, int in_bytes, int out_bytes) {
+    const int stages = 2 * in_bytes + out_bytes <= 100 * 1024 ? 2 : 1;
+    return {((d + nv - 1) / nv + 31) / 32 * 32, stages, stages * in_bytes + out_bytes};
+}
+// Rows of a tile: about 8 KB of them, whole passes of the teams, and not so many
+// that SMs stay without a tile.
+inline int odd_tile_rows(int64_t N, int row_bytes, int teams) {
+    return std::max(1, (int)std::min<int64_t>(8192 / row_bytes, N / (kSms * 4)) / teams) * teams;
 }
 
-template <class T, int MODE, bool RES, int NV, bool BLOCK, int MAXT>
-dbc_status launch_odd_res(const FwdArgs &a, cudaStream_t st) {
+template <class T, int MODE, bool RES, int NV, int MAXT>
+dbc_status launch_odd_row(const FwdArgs &a, cudaStream_t st) {
     const int slot = slot_bytes(a.d, sizeof(T));
-    const OddPlan p = odd_plan(a.N, a.d, NV, BLOCK, (RES ? 2 : 1) * slot,
-                               slot_bytes(a.d, MODE != kPlain ? 1 : a.y_bf16 ? 2 : 4));
-    auto *k = odd_kernel<T, MODE, RES, NV, BLOCK, MAXT>;
-    const int ctas = resident(k, p.threads, p.smem, (a.N + p.teams - 1) / p.teams);
+    const OddPlan p = odd_plan(a.d, NV, (RES ? 2 : 1) * slot, slot_bytes(a.d, MODE != kPlain ? 1 : a.y_bf16 ? 2 : 4));
+    auto *k = odd_kernel<T, MODE, RES, NV, MAXT>;
+    const int ctas = resident(k, p.threads, p.smem, a.N);
     if (!ctas) return DBC_ERR_CUDA;
-    k<<<ctas, p.threads, p.smem, st>>>(a, slot, p.stages, p.team_bytes);
+    k<<<ctas, p.threads, p.smem, st>>>(a, slot, p.stages);
     return DBC_OK;
 }
-template <class T, int MODE, int NV, bool BLOCK, int MAXT>
+template <class T, int MODE, bool RES, int W>
+dbc_status launch_odd_tile(const FwdArgs &a, cudaStream_t st) {
+    constexpr int TEAMS = kThreads / W;
+    const int slot = slot_bytes(a.d, sizeof(T)), oslot = slot_bytes(a.d, MODE != kPlain ? 1 : a.y_bf16 ? 2 : 4);
+    const int R = odd_tile_rows(a.N, a.d * (int)sizeof(T), TEAMS);
+    constexpr int IN = RES ? 2 : 1;
+    const int smem = R * ((2 * IN + (RES && a.s ? 1 : 0)) * slot + oslot) + a.d * 4;
+    auto *k = odd_tile_kernel<T, MODE, RES, W>;
+    const int ctas = resident(k, kThreads, smem, (a.N + R - 1) / R);
+    if (!ctas) return DBC_ERR_CUDA;
+    k<<<ctas, kThreads, smem, st>>>(a, R, slot, oslot, 2);
+    return DBC_OK;
+}
+template <class T, int MODE, bool RES>
+dbc_status launch_odd_res(const FwdArgs &a, cudaStream_t st) {
+    if (a.d <= 64) return launch_odd_tile<T, MODE, RES, 8>(a, st);
+    if (a.d <= 128) return launch_odd_tile<T, MODE, RES, 16>(a, st);
+    if (a.d <= 1024) return launch_odd_tile<T, MODE, RES, 32>(a, st);
+    if (a.d <= 2048) return launch_odd_row<T, MODE, RES, 8, 256>(a, st);
+    return launch_odd_row<T, MODE, RES, 16, 1024>(a, st);
+}
+template <class T, int MODE>
 dbc_status launch_odd(const FwdArgs &a, cudaStream_t st) {
     if constexpr (norms(MODE)) {
-        if (a.res) return launch_odd_res<T, MODE, true, NV, BLOCK, MAXT>(a, st);
+        if (a.res) return launch_odd_res<T, MODE, true>(a, st);
     }
-    return launch_odd_res<T, MODE, false, NV, BLOCK, MAXT>(a, st);
+    return launch_odd_res<T, MODE, false>(a, st);
 }
 
 // Several rows per team pay once every SM has work without them.
@@ -588,12 +608,7 @@ dbc_status launch_rows(const FwdArgs &a, cudaStream_t st) {
     const bool vec = a.d % E == 0 && on_grid(a.x, a.xs, e, 16) && on_grid(a.res, a.rs, e, 16) &&
                      on_grid(a.s, a.ss, e, 16) && on_grid(a.y, a.ys, ysz, std::min<int64_t>(16, E * ysz)) &&
                      on_grid(a.q, a.qs, 1, E) && on_grid(a.w.p, 0, 1, a.w.bf16 ? E * 2 : 16);
-    if (!vec) {
-        if (a.d <= 256) return launch_odd<T, MODE, 8, false, kThreads>(a, st);
-        if (a.d <= 512) return launch_odd<T, MODE, 16, false, kThreads>(a, st);
-        if (a.d <= 2048) return launch_odd<T, MODE, 8, true, 256>(a, st);
-        return launch_odd<T, MODE, 16, true, 1024>(a, st);
-    }
+    if (!vec) return launch_odd<T, MODE>(a, st);
     const int V = a.d / E;
     if (V <= 8)
         return many(a.N, 8, 4) ? launch_team<T, E, MODE, 8, 1, 4>(a, st) : launch_team<T, E, MODE, 8, 1, 1>(a, st);
@@ -633,15 +648,23 @@ int launch_resident(K kernel, const BwdArgs &a, int threads, int smem, int64_t m
     return ctas;
 }
 
-template <class TY, class T, int NV, bool BLOCK, int MAXT>
-int launch_odd_bwd(const BwdArgs &a, cudaStream_t st) {
+template <class TY, class T, int NV, int MAXT>
+int launch_odd_bwd_row(const BwdArgs &a, cudaStream_t st) {
     const int yslot = slot_bytes(a.d, sizeof(TY)), slot = slot_bytes(a.d, sizeof(T));
-    OddPlan p = odd_plan(a.N, a.d, NV, BLOCK, yslot + (a.ds ? 2 : 1) * slot, 0);
-    if (!BLOCK) p.smem = std::max(p.smem, kThreads / 32 * a.d * 4);       // the warps' lines of dw sums
-    const int64_t most = std::min<int64_t>(bwd_lines(a.N, a.d), (a.N + p.teams - 1) / p.teams);
-    auto *k = a.part ? odd_bwd_kernel<TY, T, true, NV, BLOCK, MAXT> : odd_bwd_kernel<TY, T, false, NV, BLOCK, MAXT>;
-    const int ctas = resident(k, p.threads, p.smem, most);
-    if (ctas) k<<<ctas, p.threads, p.smem, st>>>(a, yslot, slot, p.stages, p.team_bytes);
+    const OddPlan p = odd_plan(a.d, NV, yslot + (a.ds ? 2 : 1) * slot, 0);
+    auto *k = a.part ? odd_bwd_kernel<TY, T, true, NV, MAXT> : odd_bwd_kernel<TY, T, false, NV, MAXT>;
+    const int ctas = resident(k, p.threads, p.smem, bwd_lines(a.N, a.d));
+    if (ctas) k<<<ctas, p.threads, p.smem, st>>>(a, yslot, slot, p.stages);
+    return ctas;
+}
+template <class TY, class T, int W, int NV>
+int launch_odd_bwd_tile(const BwdArgs &a, cudaStream_t st) {
+    const int yslot = slot_bytes(a.d, sizeof(TY)), slot = slot_bytes(a.d, sizeof(T));
+    const int R = odd_tile_rows(a.N, a.d * (int)sizeof(T), kThreads / W);
+    const int smem = R * (2 * (yslot + (a.ds ? 2 : 1) * slot) + slot);
+    auto *k = a.part ? odd_bwd_tile_kernel<TY, T, true, W, NV> : odd_bwd_tile_kernel<TY, T, false, W, NV>;
+    const int ctas = resident(k, kThreads, smem, std::min<int64_t>(bwd_lines(a.N, a.d), (a.N + R - 1) / R));
+    if (ctas) k<<<ctas, kThreads, smem, st>>>(a, R, yslot, slot);
     return ctas;
 }
 
@@ -670,9 +693,12 @@ int launch_bwd(const BwdArgs &a, cudaStream_t st) {
                      on_grid(a.dx, a.xs, e, 16) && on_grid(a.dy, a.ys, ey, std::min<int64_t>(16, E * ey)) &&
                      on_grid(a.w.p, 0, 1, a.w.bf16 ? E * 2 : 16);
     if (!vec) {
-        if (a.d <= 256) return launch_odd_bwd<TY, T, 8, false, kThreads>(a, st);
-        if (a.d <= 2048) return launch_odd_bwd<TY, T, 8, true, 256>(a, st);
-        return launch_odd_bwd<TY, T, 16, true, 1024>(a, st);
+        if (a.d <= 64) return launch_odd_bwd_tile<TY, T, 8, 8>(a, st);
+        if (a.d <= 128) return launch_odd_bwd_tile<TY, T, 16, 8>(a, st);
+        if (a.d <= 256) return launch_odd_bwd_tile<TY, T, 32, 8>(a, st);
+        if (a.d <= 512) return launch_odd_bwd_tile<TY, T, 32, 16>(a, st);
+        if (a.d <= 2048) return launch_odd_bwd_row<TY, T, 8, 256>(a, st);
+        return launch_odd_bwd_row<TY, T, 16, 1024>(a, st);
     }
     const int V = a.d / E;
     if (V <= 8) return launch_bwd_team<TY, T, E, 8, 1>(a, st);
