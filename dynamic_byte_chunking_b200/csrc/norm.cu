@@ -16,45 +16,51 @@
 namespace dbc {
 namespace nm {
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // One row from registers to memory (s, then y or q), fragment column `col`.
 template <class T, int NE, int MODE, bool RES>
 __device__ __forceinline__ void write_frag(const FwdArgs &a, int64_t r, int col, const Frag<T, NE> &f,
                                            const float (&w)[NE], const RowFactor &k, const Quant &qn) {
     if (RES && a.s) f.store(static_cast<T *>(a.s) + r * a.ss + col);
-    if (MODE == kPlain) {
-        float o[NE];
+    float o[NE];
 #pragma unroll
-        for (int i = 0; i < NE; ++i) o[i] = f.at(i) * k.pre * k.rstd * w[i];
-        store_as<NE>(a.y, a.y_bf16, r * a.ys + col, o);
-    } else {
-        float p[NE];
-#pragma unroll
-        for (int i = 0; i < NE; ++i) p[i] = weighs(MODE) ? f.at(i) * w[i] : f.at(i);
-        qn.template store<narrow<T>(MODE), NE>(a.q + r * a.qs + col, p);
+    for (int i = 0; i < NE / 2; ++i) {
+        const float2 wi = make_float2(w[2 * i], w[2 * i + 1]);
+        float2 v = f.pair(i);
+        if (MODE == kPlain) {
+            if (k.pre != 1.f) v = mul2(v, both(k.pre));
+            v = mul2(mul2(v, both(k.rstd)), wi);
+        } else if (weighs(MODE)) {
+            v = mul2(v, wi);
+        }
+        o[2 * i] = v.x, o[2 * i + 1] = v.y;
     }
+    if (MODE == kPlain) store_as<NE>(a.y, a.y_bf16, r * a.ys + col, o);
+    else qn.template store<narrow<T>(MODE), NE>(a.q + r * a.qs + col, o);
 }
 
-template <class T, int NE>
-__device__ __forceinline__ void add_frag(Frag<T, NE> &f, const Frag<T, NE> &g) {
-    float v[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) v[i] = f.at(i) + g.at(i);
-    f.set(v);
-}
-
+// Sum of squares (two chains) and largest |p| of a fragment.
 template <int MODE, class T, int NE>
-__device__ __forceinline__ void stats(const Frag<T, NE> &f, const float (&w)[NE], float &ss, float &m) {
+__device__ __forceinline__ void stats(const Frag<T, NE> &f, const float (&w)[NE], float2 &ss, float &m) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const float v = f.at(i);
-        if (norms(MODE)) ss = fmaf(v, v, ss);
-        if (MODE != kPlain) m = abs_max(m, weighs(MODE) ? v * w[i] : v);
+    for (int i = 0; i < NE / 2; ++i) {
+        const float2 v = f.pair(i);
+        if (norms(MODE)) ss = fma2(v, v, ss);
+        if (MODE != kPlain) m = abs_max(m, weighs(MODE) ? mul2(v, make_float2(w[2 * i], w[2 * i + 1])) : v);
     }
+}
+
+// Rows in shared memory at a time of kernels that copy ahead: B bytes per thread and row, up to MAXT
+// threads; 64 KB a CTA of 256 threads (three to an SM), and what fits for the wide ones.
+constexpr int block_stages(int B, int MAXT) {
+    const int s = MAXT > 256 ? 200 * 1024 / (B * MAXT) : 64 * 1024 / (B * MAXT);
+    return s < 1 ? 1 : s > 4 ? 4 : s;
 }
 
 // R rows per team of W lanes, NV fragments per lane and row.
 template <class T, int NE, int MODE, bool RES, int W, int NV, int R>
-__global__ void __launch_bounds__(kThreads) team_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) team_kernel(const FwdArgs a) {
     const int64_t team = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / W;
     const int t = threadIdx.x % W;
     if ((((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) / W) * R >= a.N) return;   // a whole warp
@@ -71,24 +77,25 @@ __global__ void __launch_bounds__(kThreads) team_kernel(const FwdArgs a) {
                 if (RES) g[i][j].load(static_cast<const T *>(a.res) + (r0 + i) * a.rs + col);
             }
         }
+    constexpr bool LATE = MODE == kPlain && NV > 2;          // the weight, where registers are short
     float w[NV][NE];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int col = (j * W + t) * NE;
 #pragma unroll
         for (int i = 0; i < NE; ++i) w[j][i] = 1.f;
-        if (norms(MODE) && col < a.d) a.w.get<NE>(col, w[j]);
+        if (norms(MODE) && !LATE && col < a.d) a.w.get<NE>(col, w[j]);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        float ss = 0.f;
+        float2 s2 = make_float2(0.f, 0.f);
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (RES && r0 + i < a.N && (j * W + t) * NE < a.d) add_frag(f[i][j], g[i][j]);
-            stats<MODE>(f[i][j], w[j], ss, m);
+            if (RES && r0 + i < a.N && (j * W + t) * NE < a.d) f[i][j].add(g[i][j]);
+            stats<MODE>(f[i][j], w[j], s2, m);
         }
-        if (norms(MODE)) ss = team_reduce<W>(ss, Add());
+        const float ss = norms(MODE) ? team_reduce<W>(s2.x + s2.y, Add()) : 1.f;
         if (MODE != kPlain) m = team_reduce<W>(m, AbsMax());
         RowFactor k(ss, a.d, a.eps);
         if (norms(MODE) && __any_sync(0xffffffffu, !(ss >= kLow && ss <= kHigh))) {
@@ -109,6 +116,7 @@ __global__ void __launch_bounds__(kThreads) team_kernel(const FwdArgs a) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int col = (j * W + t) * NE;
+                if (LATE && col < a.d) a.w.get<NE>(col, w[j]);
                 if (col < a.d) write_frag<T, NE, MODE, RES>(a, r0 + i, col, f[i][j], w[j], k, qn);
             }
             if (MODE != kPlain && t == 0) {
@@ -119,48 +127,107 @@ __global__ void __launch_bounds__(kThreads) team_kernel(const FwdArgs a) {
     }
 }
 
-// One row per CTA of blockDim.x threads (a multiple of 32), NV fragments each.
-template <class T, int NE, int MODE, bool RES, int NV>
-__global__ void __launch_bounds__(1024) block_kernel(const FwdArgs a) {
-    __shared__ float s_ss[32];
-    __shared__ float s_m[32];
-    __shared__ double s_t[32];
+// Rows on their way to a thread: the fragments that it will work on, copied by itself into its own slots
+// of shared memory some rows ahead (cp.async; nobody else reads them, so no barrier).  An array's
+// fragments are `threads` 16-byte units (or one smaller unit) apart, so that a warp's accesses are whole
+// lines; `at` is the offset per thread of the fragment inside a stage.
+template <int NE, class V>
+__device__ __forceinline__ void ring_copy(uint32_t stage, int at, int threads, const V *src, bool in) {
+    constexpr int bytes = NE * (int)sizeof(V), u = bytes < 16 ? bytes : 16;
+    const uint32_t dst = stage + at * threads + threadIdx.x * u;
+    if constexpr (bytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < bytes / 16; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * threads * 16),
+                         "l"(reinterpret_cast<const char *>(src) + i * 16), "r"(in ? 16 : 0)
+                         : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(in ? bytes : 0), "n"(bytes)
+                     : "memory");
+    }
+}
+template <int NE, class V>
+__device__ __forceinline__ void ring_read(Frag<V, NE> &f, const char *stage, int at, int threads) {
+    constexpr int bytes = NE * (int)sizeof(V), u = bytes < 16 ? bytes : 16;
+    const char *p = stage + at * threads + threadIdx.x * u;
+    uint32_t w[bytes / 4];
+    if constexpr (u == 16) {
+#pragma unroll
+        for (int i = 0; i < bytes / 16; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p + i * threads * 16);
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    }
+    f.from_words(w);
+}
+template <int S>
+__device__ __forceinline__ void ring_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+}
+
+// Wide rows, forward: CTAs of blockDim.x threads walk the rows, NV fragments of one row per thread, the
+// next S - 1 rows on their way.
+template <class T, int NE, int MODE, bool RES, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_kernel(const FwdArgs a) {
+    constexpr int U = NE * (int)sizeof(T), B = NV * U * (RES ? 2 : 1);       // bytes of a fragment, of a thread's row
+    constexpr int S = block_stages(B, MAXT);
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float2 part[2][32];
+    __shared__ double wide[32];
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     const int t = threadIdx.x, W = blockDim.x, lane = t & 31, warp = t >> 5, warps = W >> 5;
-    for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
-        Frag<T, NE> f[NV], g[NV];
+    auto start = [&](int64_t r, int st) {
+        const bool row = r < a.N;
+        const T *const x = static_cast<const T *>(a.x) + (row ? r : 0) * a.xs;
+        const T *const g = RES ? static_cast<const T *>(a.res) + (row ? r : 0) * a.rs : x;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (j * W + t) * NE;
-            f[j].zero();
-            if (col < a.d) {
-                f[j].load(static_cast<const T *>(a.x) + r * a.xs + col);
-                if (RES) g[j].load(static_cast<const T *>(a.res) + r * a.rs + col);
-            }
+            const bool in = row && col < a.d;
+            ring_copy<NE>(base + st * B * W, j * U, W, x + (in ? col : 0), in);
+            if (RES) ring_copy<NE>(base + st * B * W, (NV + j) * U, W, g + (in ? col : 0), in);
         }
-        float w[NV][NE];
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int k = 0; k < S - 1; ++k) start(blockIdx.x + (int64_t)k * gridDim.x, k);
+    // The weight stays in registers, but in the plain norm of up to 512 fragments, which does better
+    // with more warps than with them (20000 x 4096: 105 us against 114; 8192 x 8192: 99 against 96).
+    constexpr bool LATE = MODE == kPlain && MAXT <= 256;
+    float w[NV][NE];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (j * W + t) * NE;
+    for (int j = 0; j < NV; ++j) {
+        const int col = (j * W + t) * NE;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) w[j][i] = 1.f;
-            if (norms(MODE) && col < a.d) a.w.get<NE>(col, w[j]);
-        }
-        float ss = 0.f;
+        for (int i = 0; i < NE; ++i) w[j][i] = 1.f;
+        if (norms(MODE) && !LATE && col < a.d) a.w.get<NE>(col, w[j]);
+    }
+    int ph = 0, st = 0;
+    for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, ph ^= 1) {
+        start(r + (int64_t)(S - 1) * gridDim.x, st == 0 ? S - 1 : st - 1);
+        ring_wait<S>();
+        Frag<T, NE> f[NV];
+        float2 s2 = make_float2(0.f, 0.f);
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (RES && (j * W + t) * NE < a.d) add_frag(f[j], g[j]);
-            stats<MODE>(f[j], w[j], ss, m);
+            ring_read<NE>(f[j], smem + st * B * W, j * U, W);
+            if constexpr (RES) {
+                Frag<T, NE> g;
+                ring_read<NE>(g, smem + st * B * W, (NV + j) * U, W);
+                f[j].add(g);                             // zeros past the row's end
+            }
+            stats<MODE>(f[j], w[j], s2, m);
         }
-        if (norms(MODE)) ss = team_reduce<32>(ss, Add());
+        float ss = norms(MODE) ? team_reduce<32>(s2.x + s2.y, Add()) : 0.f;
         if (MODE != kPlain) m = team_reduce<32>(m, AbsMax());
-        if (lane == 0) {
-            s_ss[warp] = ss;
-            s_m[warp] = m;
-        }
-        __syncthreads();
-        if (norms(MODE)) ss = team_reduce<32>(lane < warps ? s_ss[lane] : 0.f, Add());
-        if (MODE != kPlain) m = team_reduce<32>(lane < warps ? s_m[lane] : 0.f, AbsMax());
+        if (lane == 0) part[ph][warp] = make_float2(ss, m);
+        __syncthreads();             // the other buffer's readers are past the row before's barrier
+        const float2 v = lane < warps ? part[ph][lane] : make_float2(0.f, 0.f);
+        if (norms(MODE)) ss = team_reduce<32>(v.x, Add());
+        if (MODE != kPlain) m = team_reduce<32>(v.y, AbsMax());
         RowFactor k(ss, a.d, a.eps);
         if (norms(MODE) && !(ss >= kLow && ss <= kHigh)) {     // the same in every thread
             double t2 = 0;
@@ -169,9 +236,9 @@ __global__ void __launch_bounds__(1024) block_kernel(const FwdArgs a) {
 #pragma unroll
                 for (int e = 0; e < NE; ++e) t2 += (double)f[j].at(e) * f[j].at(e);
             t2 = team_reduce<32>(t2, Add());
-            if (lane == 0) s_t[warp] = t2;
+            if (lane == 0) wide[warp] = t2;
             __syncthreads();
-            t2 = team_reduce<32>(lane < warps ? s_t[lane] : 0.0, Add());
+            t2 = team_reduce<32>(lane < warps ? wide[lane] : 0.0, Add());
             k = RowFactor(t2, a.d, a.eps);
             if (!isfinite(t2)) {
                 m = __int_as_float(0x7fc00000);
@@ -182,104 +249,62 @@ __global__ void __launch_bounds__(1024) block_kernel(const FwdArgs a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (j * W + t) * NE;
-            if (col < a.d) write_frag<T, NE, MODE, RES>(a, r, col, f[j], w[j], k, qn);
+            if (col < a.d) {
+                if (LATE) a.w.get<NE>(col, w[j]);
+                write_frag<T, NE, MODE, RES>(a, r, col, f[j], w[j], k, qn);
+            }
         }
         if (MODE != kPlain && t == 0) {
             a.scale[r] = row_scale<MODE>(qn, k);
             if (qn.bad) flag(a.st, DBC_ERR_NONFINITE);
         }
-        if (r + gridDim.x < a.N) __syncthreads();      // the shared words are written again
+        if (++st == S) st = 0;
     }
 }
 
-// Rows on their way to a thread: the fragments of dy, s and ds that it will work on, copied by itself
-// into its own slots of shared memory S rows ahead (cp.async; nobody else reads them, so no barrier).
+// The same for the backward pass: dy, s and ds of a thread's row.
 template <class TY, class T, int NE, int NV, int MAXT>
 struct Ring {
-    static constexpr int B = NV * NE * (int)(sizeof(TY) + 2 * sizeof(T));       // a thread's bytes of a row, with ds
-    static constexpr int S = MAXT > 256 ? (B * 2 * MAXT <= 200 * 1024 ? 2 : 1) : B <= 48 ? 4 : B <= 64 ? 3 : 2;
-    static constexpr int kS = NV * NE * (int)sizeof(TY), kDs = kS + NV * NE * (int)sizeof(T);
+    static constexpr int UY = NE * (int)sizeof(TY), U = NE * (int)sizeof(T), kS = NV * UY, kDs = kS + NV * U;
+    static constexpr int B = kDs + NV * U, S = block_stages(B, MAXT);
     static constexpr int smem(int threads) { return S * B * threads; }
-
-    template <class V>
-    static __device__ __forceinline__ void copy(uint32_t dst, const V *src, bool in, int threads) {
-        constexpr int bytes = NE * (int)sizeof(V);
-        if constexpr (bytes >= 16) {
-#pragma unroll
-            for (int i = 0; i < bytes / 16; ++i)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * threads * 16),
-                             "l"(reinterpret_cast<const char *>(src) + i * 16), "r"(in ? 16 : 0)
-                             : "memory");
-        } else {
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(in ? bytes : 0),
-                         "n"(bytes)
-                         : "memory");
-        }
-    }
     // Starts the copies of row r (nothing, but still a group, when r is past the end).
     static __device__ __forceinline__ void start(const BwdArgs &a, uint32_t base, int stage, int64_t r, int t, int W,
                                                  int threads) {
-        {
-            const uint32_t st = base + stage * B * threads;
-            const bool row = r < a.N;
-            const int64_t rr = row ? r : 0;
+        const uint32_t st = base + stage * B * threads;
+        const bool row = r < a.N;
+        const int64_t rr = row ? r : 0;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = (j * W + t) * NE;
-                const bool in = row && col < a.d;
-                const int c = in ? col : 0;
-                constexpr int uy = NE * (int)sizeof(TY) < 16 ? NE * (int)sizeof(TY) : 16;
-                constexpr int us = NE * (int)sizeof(T) < 16 ? NE * (int)sizeof(T) : 16;
-                const int me = threadIdx.x;
-                copy(st + (j * NE * (int)sizeof(TY)) * threads + me * uy, static_cast<const TY *>(a.dy) + rr * a.ys + c, in,
-                     threads);
-                copy(st + (kS + j * NE * (int)sizeof(T)) * threads + me * us, static_cast<const T *>(a.s) + rr * a.ss + c,
-                     in, threads);
-                if (a.ds)
-                    copy(st + (kDs + j * NE * (int)sizeof(T)) * threads + me * us,
-                         static_cast<const T *>(a.ds) + rr * a.ds_s + c, in, threads);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int j = 0; j < NV; ++j) {
+            const int col = (j * W + t) * NE;
+            const bool in = row && col < a.d;
+            const int c = in ? col : 0;
+            ring_copy<NE>(st, j * UY, threads, static_cast<const TY *>(a.dy) + rr * a.ys + c, in);
+            ring_copy<NE>(st, kS + j * U, threads, static_cast<const T *>(a.s) + rr * a.ss + c, in);
+            if (a.ds) ring_copy<NE>(st, kDs + j * U, threads, static_cast<const T *>(a.ds) + rr * a.ds_s + c, in);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    static __device__ __forceinline__ void wait() {
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-    }
-    template <class V>
-    static __device__ __forceinline__ void read(Frag<V, NE> &f, const char *smem, int at, int threads) {
-        constexpr int bytes = NE * (int)sizeof(V), u = bytes < 16 ? bytes : 16;
-        const char *p = smem + at * threads + threadIdx.x * u;
-        uint32_t w[bytes / 4 ? bytes / 4 : 1];
-        if constexpr (u == 16) {
-#pragma unroll
-            for (int i = 0; i < bytes / 16; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(p + i * threads * 16);
-                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-            }
-        } else if constexpr (u == 8) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(p);
-            w[0] = x.x, w[1] = x.y;
-        }
-        f.from_words(w);
-    }
-    // Fragment j of row r's dy and s; then of its ds.
-    static __device__ __forceinline__ void get(const char *smem, int stage, int j, int threads, Frag<TY, NE> &y, Frag<T, NE> &f) {
-        const char *st = smem + stage * B * threads;
-        read(y, st, j * NE * (int)sizeof(TY), threads);
-        read(f, st, kS + j * NE * (int)sizeof(T), threads);
+    static __device__ __forceinline__ void wait() { ring_wait<S>(); }
+    // Fragment j of the row's dy and s; then of its ds.
+    static __device__ __forceinline__ void get(const char *smem, int stage, int j, int threads, Frag<TY, NE> &y,
+                                               Frag<T, NE> &f) {
+        ring_read<NE>(y, smem + stage * B * threads, j * UY, threads);
+        ring_read<NE>(f, smem + stage * B * threads, kS + j * U, threads);
     }
     static __device__ __forceinline__ void get_ds(const char *smem, int stage, int j, int threads, Frag<T, NE> &g) {
-        read(g, smem + stage * B * threads, kDs + j * NE * (int)sizeof(T), threads);
+        ring_read<NE>(g, smem + stage * B * threads, kDs + j * U, threads);
     }
 };
 
 template <class TY, class T, int NE>
 __device__ __forceinline__ void bwd_stats(const Frag<TY, NE> &y, const Frag<T, NE> &f, const float (&w)[NE],
-                                          float &ss, float &sg) {
+                                          float2 &ss, float2 &sg) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        ss = fmaf(f.at(i), f.at(i), ss);
-        sg = fmaf(y.at(i) * w[i], f.at(i), sg);
+    for (int i = 0; i < NE / 2; ++i) {
+        const float2 v = f.pair(i);
+        ss = fma2(v, v, ss);
+        sg = fma2(mul2(y.pair(i), make_float2(w[2 * i], w[2 * i + 1])), v, sg);
     }
 }
 template <class TY, class T, int NE>
@@ -300,17 +325,28 @@ __device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int
                                          int threads, const Frag<TY, NE> &y, const Frag<T, NE> &f,
                                          const float (&w)[NE], const BwdFactor &k, float (&acc)[NE]) {
     float o[NE];
+    const bool scaled = k.k.pre != 1.f;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const float xh = f.at(i) * k.k.pre * k.k.rstd;
-        o[i] = fmaf(-xh, k.c, y.at(i) * w[i]) * k.k.rstd * k.k.pre;
-        if (DW) acc[i] = fmaf(y.at(i), xh, acc[i]);
+    for (int i = 0; i < NE / 2; ++i) {
+        const float2 wi = make_float2(w[2 * i], w[2 * i + 1]), yi = y.pair(i);
+        float2 xh = mul2(f.pair(i), both(k.k.rstd));
+        if (scaled) xh = mul2(mul2(f.pair(i), both(k.k.pre)), both(k.k.rstd));
+        float2 v = mul2(fma2(xh, both(-k.c), mul2(yi, wi)), both(k.k.rstd));
+        if (scaled) v = mul2(v, both(k.k.pre));
+        o[2 * i] = v.x, o[2 * i + 1] = v.y;
+        if (DW) {
+            const float2 s2 = fma2(yi, xh, make_float2(acc[2 * i], acc[2 * i + 1]));
+            acc[2 * i] = s2.x, acc[2 * i + 1] = s2.y;
+        }
     }
     Frag<T, NE> q;
     if (a.ds) {
         Q::get_ds(smem, stage, j, threads, q);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) o[i] += q.at(i);
+        for (int i = 0; i < NE / 2; ++i) {
+            const float2 v = add2(make_float2(o[2 * i], o[2 * i + 1]), q.pair(i));
+            o[2 * i] = v.x, o[2 * i + 1] = v.y;
+        }
     }
     q.set(o);
     q.store(static_cast<T *>(a.dx) + r * a.xs + col);
@@ -343,13 +379,12 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
         Q::wait();
         Frag<TY, NE> y[NV];
         Frag<T, NE> f[NV];
-        float ss = 0.f, sg = 0.f;
+        float2 pss = make_float2(0.f, 0.f), psg = pss;
 #pragma unroll
         for (int j = 0; j < NV; ++j) Q::get(smem, stage, j, kThreads, y[j], f[j]);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], ss, sg);
-        ss = team_reduce<W>(ss, Add());
-        sg = team_reduce<W>(sg, Add());
+        for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], pss, psg);
+        const float ss = team_reduce<W>(pss.x + pss.y, Add()), sg = team_reduce<W>(psg.x + psg.y, Add());
         BwdFactor k(ss, sg, a.d, a.eps);
         if (__any_sync(0xffffffffu, !in_range(ss, sg))) {
             double s2 = 0, g2 = 0;
@@ -369,7 +404,12 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
         if (++stage == Q::S) stage = 0;
     }
     if constexpr (DW) {
-        __shared__ float sm[kThreads / 32][NV * W * NE];
+        // the ring's room, a line per warp (a stage alone holds at least 4 bytes per column and warp)
+        constexpr int LINE = NV * W * NE;
+        static_assert(Q::smem(kThreads) >= kThreads / 32 * LINE * 4, "");
+        float *const sm = reinterpret_cast<float *>(smem);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -377,13 +417,13 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
                 float v = acc[j][i];
 #pragma unroll
                 for (int o = W; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane < W) sm[warp][(j * W + t) * NE + i] = v;
+                if (lane < W) sm[warp * LINE + (j * W + t) * NE + i] = v;
             }
         __syncthreads();
         for (int c = threadIdx.x; c < a.d; c += kThreads) {
             float v = 0.f;
 #pragma unroll
-            for (int k = 0; k < kThreads / 32; ++k) v += sm[k][c];
+            for (int k = 0; k < kThreads / 32; ++k) v += sm[k * LINE + c];
             a.part[(int64_t)blockIdx.x * a.d + c] = v;
         }
     }
@@ -413,13 +453,12 @@ __global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
         Q::wait();
         Frag<TY, NE> y[NV];
         Frag<T, NE> f[NV];
-        float ss = 0.f, sg = 0.f;
+        float2 pss = make_float2(0.f, 0.f), psg = pss;
 #pragma unroll
         for (int j = 0; j < NV; ++j) Q::get(smem, stage, j, W, y[j], f[j]);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], ss, sg);
-        ss = team_reduce<32>(ss, Add());
-        sg = team_reduce<32>(sg, Add());
+        for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], pss, psg);
+        float ss = team_reduce<32>(pss.x + pss.y, Add()), sg = team_reduce<32>(psg.x + psg.y, Add());
         if (lane == 0) part[ph][warp] = make_float2(ss, sg);
         __syncthreads();             // the other buffer's readers are past the row before's barrier
         const float2 v = lane < warps ? part[ph][lane] : make_float2(0.f, 0.f);
@@ -519,20 +558,6 @@ dbc_status launch_team(const FwdArgs &a, cudaStream_t st) {
     return DBC_OK;
 }
 
-template <class T, int NE, int MODE, int NV>
-dbc_status launch_block(const FwdArgs &a, cudaStream_t st) {
-    const int threads = ((a.d + NE * NV - 1) / (NE * NV) + 31) / 32 * 32;
-    const unsigned grid = (unsigned)std::min<int64_t>(a.N, INT32_MAX);
-    if constexpr (norms(MODE)) {
-        if (a.res) {
-            block_kernel<T, NE, MODE, true, NV><<<grid, threads, 0, st>>>(a);
-            return DBC_OK;
-        }
-    }
-    block_kernel<T, NE, MODE, false, NV><<<grid, threads, 0, st>>>(a);
-    return DBC_OK;
-}
-
 // As many CTAs as are resident at once, at most `most`; 0 after a CUDA error.
 constexpr int kSms = 148;
 template <class K>
@@ -542,6 +567,24 @@ int resident(K kernel, int threads, int smem, int64_t most) {
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
         return 0;
     return (int)std::min<int64_t>(most, (int64_t)per_sm * kSms);
+}
+
+template <class T, int NE, int MODE, bool RES, int NV, int MAXT>
+dbc_status launch_block_res(const FwdArgs &a, cudaStream_t st) {
+    constexpr int B = NV * NE * (int)sizeof(T) * (RES ? 2 : 1);
+    const int threads = ((a.d + NE * NV - 1) / (NE * NV) + 31) / 32 * 32, smem = block_stages(B, MAXT) * B * threads;
+    auto *k = block_kernel<T, NE, MODE, RES, NV, MAXT>;
+    const int ctas = resident(k, threads, smem, a.N);
+    if (!ctas) return DBC_ERR_CUDA;
+    k<<<ctas, threads, smem, st>>>(a);
+    return DBC_OK;
+}
+template <class T, int NE, int MODE, int NV, int MAXT>
+dbc_status launch_block(const FwdArgs &a, cudaStream_t st) {
+    if constexpr (norms(MODE)) {
+        if (a.res) return launch_block_res<T, NE, MODE, true, NV, MAXT>(a, st);
+    }
+    return launch_block_res<T, NE, MODE, false, NV, MAXT>(a, st);
 }
 
 // Threads, rows in shared memory (two where that leaves room for a second CTA)
@@ -619,8 +662,12 @@ dbc_status launch_rows(const FwdArgs &a, cudaStream_t st) {
     if (V <= 64)
         return many(a.N, 32, 2) ? launch_team<T, E, MODE, 32, 2, 2>(a, st) : launch_team<T, E, MODE, 32, 2, 1>(a, st);
     if (V <= 128) return launch_team<T, E, MODE, 32, 4, 1>(a, st);
-    if (V <= 2048) return launch_block<T, E, MODE, 2>(a, st);
-    return launch_block<T, E, MODE, 4>(a, st);
+    if (V <= 512) return launch_block<T, E, MODE, 2, 256>(a, st);
+    if (V <= 1024) return launch_block<T, E, MODE, 2, 512>(a, st);
+    if constexpr (sizeof(T) == 4) {
+        if (V > 2048) return launch_block<T, E, MODE, 4, 1024>(a, st);
+    }
+    return launch_block<T, E, MODE, 2, 1024>(a, st);
 }
 
 template <int MODE>
@@ -698,6 +745,7 @@ int launch_bwd(const BwdArgs &a, cudaStream_t st) {
         if (a.d <= 256) return launch_odd_bwd_tile<TY, T, 32, 8>(a, st);
         if (a.d <= 512) return launch_odd_bwd_tile<TY, T, 32, 16>(a, st);
         if (a.d <= 2048) return launch_odd_bwd_row<TY, T, 8, 256>(a, st);
+        if (a.d <= 8192) return launch_odd_bwd_row<TY, T, 8, 1024>(a, st);
         return launch_odd_bwd_row<TY, T, 16, 1024>(a, st);
     }
     const int V = a.d / E;
@@ -706,8 +754,11 @@ int launch_bwd(const BwdArgs &a, cudaStream_t st) {
     if (V <= 32) return launch_bwd_team<TY, T, E, 32, 1>(a, st);
     if (V <= 64) return launch_bwd_team<TY, T, E, 32, 2>(a, st);
     if (V <= 512) return launch_bwd_block<TY, T, E, 2, 256>(a, st);
-    if (V <= 2048) return launch_bwd_block<TY, T, E, 2, 1024>(a, st);
-    return launch_bwd_block<TY, T, E, 4, 1024>(a, st);
+    if (V <= 1024) return launch_bwd_block<TY, T, E, 2, 512>(a, st);
+    if constexpr (sizeof(T) == 4) {
+        if (V > 2048) return launch_bwd_block<TY, T, E, 4, 1024>(a, st);
+    }
+    return launch_bwd_block<TY, T, E, 2, 1024>(a, st);
 }
 
 }  // namespace nm

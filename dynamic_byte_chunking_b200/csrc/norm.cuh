@@ -17,6 +17,15 @@ struct Frag;
 template <>
 struct Frag<__nv_bfloat16, 8> {
     uint32_t w[4];
+    __device__ __forceinline__ float2 pair(int i) const {
+        return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    // bf16(fp32(a + b)) is bf16(a + b): where the exponents are so far apart that fp32 rounds the sum,
+    // it rounds to the larger operand either way.
+    __device__ __forceinline__ void add(const Frag &g) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(g.w[i]));
+    }
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
         const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(p));
         w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
@@ -48,6 +57,15 @@ struct Frag<__nv_bfloat16, 8> {
 template <>
 struct Frag<__nv_bfloat16, 4> {
     uint32_t w[2];
+    __device__ __forceinline__ float2 pair(int i) const {
+        return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    // bf16(fp32(a + b)) is bf16(a + b): where the exponents are so far apart that fp32 rounds the sum,
+    // it rounds to the larger operand either way.
+    __device__ __forceinline__ void add(const Frag &g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(g.w[i]));
+    }
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
         const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(p));
         w[0] = u.x, w[1] = u.y;
@@ -93,6 +111,11 @@ template <int NE>
 struct Frag<float, NE> {
     static_assert(NE == 8 || NE == 4 || NE == 1, "");
     float v[NE];
+    __device__ __forceinline__ float2 pair(int i) const { return make_float2(v[2 * i], v[2 * i + 1]); }
+    __device__ __forceinline__ void add(const Frag &g) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] += g.v[i];
+    }
     __device__ __forceinline__ void load(const float *p) {
         if constexpr (NE == 1) {
             v[0] = __ldcg(p);
@@ -182,6 +205,12 @@ __device__ __forceinline__ float abs_max(float m, float v) {
     return r;
 }
 
+__device__ __forceinline__ float abs_max(float m, float2 v) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(v.x), "f"(v.y));
+    return r;
+}
+
 // How a row is quantised, from its m = max |p|.
 //
 // The code is rint(127 p / m), halves to even, and it has to be the exact
@@ -246,18 +275,15 @@ struct Quant {
                 u[i + 1] = __float_as_uint(settle<NARROW>(p[i + 1], ms, v.y, t.y));
             }
         }
-        if (bad) {
-#pragma unroll
-            for (int i = 0; i < NE; ++i) u[i] = 0;
-        }
         if constexpr (NE == 1) {
-            *q = (int8_t)u[0];
+            *q = bad ? (int8_t)0 : (int8_t)u[0];
         } else {
             uint32_t w[NE / 4];
 #pragma unroll
             for (int i = 0; i < NE / 4; ++i)
-                w[i] = __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040),
-                                   __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040), 0x5410);
+                w[i] = bad ? 0u
+                           : __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040),
+                                         __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040), 0x5410);
             if constexpr (NE == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
             else *reinterpret_cast<uint32_t *>(q) = w[0];
         }
