@@ -325,16 +325,42 @@ template <int BT>
 struct Split {
     static constexpr int NS = BT <= 32 ? 5 : 4;
     static constexpr uint32_t W = 128 * 128, X = BT * 128, STAGE = W + X;
-    static constexpr int PITCH = 129;                                     // words per token of the partial sums
+    static constexpr int PITCH = 132;                                     // words per token of the partial sums
     static constexpr uint32_t RING = NS * STAGE, PART = BT * PITCH * 4;
     static constexpr size_t SMEM = (RING > PART ? RING : PART) + 1024;
     static constexpr int TCOLS = BT < 32 ? 32 : BT;
 };
 
-__device__ __forceinline__ int ld_cluster(uint32_t addr, uint32_t rank) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(tc::map_to(addr, rank)) : "memory");
+__device__ __forceinline__ int4 ld_cluster(uint32_t addr, uint32_t rank) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(tc::map_to(addr, rank)));
     return v;
+}
+
+// Joins the partial sums of tokens rank, rank + S, ... of a cluster of S CTAs: a warp takes a token at a
+// time, a lane four channels; four tokens' loads from all CTAs are in flight together.
+template <int S, int PITCH, class F>
+__device__ __forceinline__ void join(uint32_t base, uint32_t rank, int rows, F put) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int m0 = (int)rank + S * warp; m0 < rows; m0 += S * 16) {
+        int4 v[4][S];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < S; ++r) {
+                const int m = m0 + S * 4 * i;
+                v[i][r] = m < rows ? ld_cluster(base + (uint32_t)(m * PITCH + lane * 4) * 4u, r) : make_int4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int4 t = v[i][0];
+#pragma unroll
+            for (int r = 1; r < S; ++r) t.x += v[i][r].x, t.y += v[i][r].y, t.z += v[i][r].z, t.w += v[i][r].w;
+            if (m0 + S * 4 * i < rows) put(m0 + S * 4 * i, t);
+        }
+    }
 }
 
 template <int BT>
@@ -406,25 +432,24 @@ __global__ void __launch_bounds__(128)
     }
     __syncthreads();
     tc::fence_after_sync();
-    const int nl = tid, n = n0 + nl;                    // this thread's channel
     const int rows = min(BT, p.M - m0);
-    const float bs = n < p.N ? p.bs[n] : 0.f, bias = n < p.N ? bias_at(p, n) : 0.f;
-    auto put = [&](int m, int sum) {
-        if (n >= p.N) return;
-        const float v = fmaf((float)sum * p.as[m0 + m], bs, bias);
+    const bool ok = s_ok != 0;
+    auto put = [&](int m, int n, int sum, float as, float bs, float bias) {
+        const float v = fmaf((float)sum * as, bs, bias);
         const int64_t at = (int64_t)(m0 + m) * p.ldo + n;
         if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
         else static_cast<float *>(p.out)[at] = v;
     };
-    const bool ok = s_ok != 0;
     if (splits == 1) {
+        const int n = n0 + tid;                         // this thread's channel
+        const float bs = n < p.N ? p.bs[n] : 0.f, bias = n < p.N ? bias_at(p, n) : 0.f;
         for (int c0 = 0; c0 < rows && ok; c0 += 16) {
             uint32_t v[16];
             tc::tmem_ld16_nw(tbase + ((uint32_t)(warp * 32) << 16) + c0, v);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                if (c0 + j < rows) put(c0 + j, p.K ? (int)v[j] : 0);
+                if (c0 + j < rows && n < p.N) put(c0 + j, n, p.K ? (int)v[j] : 0, p.as[m0 + c0 + j], bs, bias);
         }
     } else {
         for (int c0 = 0; c0 < rows; c0 += 16) {
@@ -432,15 +457,29 @@ __global__ void __launch_bounds__(128)
             tc::tmem_ld16_nw(tbase + ((uint32_t)(warp * 32) << 16) + c0, v);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) part[(c0 + j) * C::PITCH + nl] = (int)v[j];
+            for (int j = 0; j < 16; ++j) part[(c0 + j) * C::PITCH + tid] = (int)v[j];
         }
+        const int n = n0 + lane * 4;                    // the first of this lane's channels
+        float bs[4], bias[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bs[j] = n + j < p.N ? p.bs[n + j] : 0.f;
+            bias[j] = n + j < p.N ? bias_at(p, n + j) : 0.f;
+        }
+        auto put4 = [&](int m, const int4 &t) {
+            const float as = p.as[m0 + m];
+            const int s[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < p.N) put(m, n + j, s[j], as, bs[j], bias[j]);
+        };
         tc::cluster_sync();
-        for (int m = (int)rank; m < rows && ok; m += splits) {
-            int sum = 0;
-            for (int r = 0; r < splits; ++r) sum += ld_cluster(base + (uint32_t)(m * C::PITCH + nl) * 4u, r);
-            put(m, sum);
+        if (ok) {
+            if (splits == 2) join<2, C::PITCH>(base, rank, rows, put4);
+            else if (splits == 4) join<4, C::PITCH>(base, rank, rows, put4);
+            else join<8, C::PITCH>(base, rank, rows, put4);
         }
-        tc::cluster_sync();                                  // the others have read this CTA's sums
+        tc::cluster_sync();                              // the others have read this CTA's sums
     }
     tc::fence_before_sync();
     __syncthreads();
