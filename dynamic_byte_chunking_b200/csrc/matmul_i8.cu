@@ -76,7 +76,7 @@ __device__ __forceinline__ Tile tile_at(int64_t i, int mt, int nt) {
     return {(int)(rem / w), g * 16 + (int)(rem % w)};
 }
 
-template <bool TMA_OUT, bool BF16>
+template <bool TMA_OUT, bool BF16, bool BIAS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                 const __grid_constant__ CUtensorMap to, const Args p) {
@@ -201,19 +201,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
         constexpr int COLS = BF16 ? 32 : 16;             // columns of a slab
         constexpr int E = COLS / 4;                      // elements of 16 bytes
         bool ok = true;
-        // The next tile's scales are fetched while this one is computed: the row's by its thread, the
-        // channels' scales by the first 256 threads, their bias by the others.
-        float as = 0.f;
+        // The next tile's scales are fetched while this one is computed: a lane's four rows' by itself,
+        // the channels' scales by the first 256 threads, their bias by the others.
+        float as[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t ch_raw = 0;
         auto fetch = [&](int64_t i) {
             if (i >= tiles) return;
             const Tile t = tile_at(i, mt, nt);
-            const int row = t.m * C::BM + (int)rank * 128 + q * 32 + lane, j = t.n * C::BN + (et & 255);
-            if (row < p.M) as = p.as[row];
+            const int row = t.m * C::BM + (int)rank * 128 + q * 32 + (lane >> 2), j = t.n * C::BN + (et & 255);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (row + h * 8 < p.M) as[h] = p.as[row + h * 8];
             if (j < p.N) {
                 if (et < 256) ch_raw = __float_as_uint(p.bs[j]);
-                else if (p.bias && p.bias_bf16) ch_raw = static_cast<const uint16_t *>(p.bias)[j];
-                else if (p.bias) ch_raw = static_cast<const uint32_t *>(p.bias)[j];
+                else if (BIAS && p.bias_bf16) ch_raw = static_cast<const uint16_t *>(p.bias)[j];
+                else if (BIAS) ch_raw = static_cast<const uint32_t *>(p.bias)[j];
             }
         };
         fetch(pair);
@@ -225,8 +227,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
             // the other buffer is still read by warps of the tile before; this one's readers are past the
             // barrier of that tile
             if (et < 256) s_scale[b][et] = __uint_as_float(ch_raw);
-            else s_bias[b][et - 256] = __uint_as_float(p.bias_bf16 ? ch_raw << 16 : ch_raw);
-            const float2 as2 = make_float2(as, as);
+            else if (BIAS) s_bias[b][et - 256] = __uint_as_float(p.bias_bf16 ? ch_raw << 16 : ch_raw);
+            const float ra[4] = {as[0], as[1], as[2], as[3]};
             asm volatile("bar.sync 1, %0;" ::"n"(C::EPI * 32) : "memory");
             fetch(i + pairs);
             // after a timeout the warps still meet at the barrier above, without work
@@ -234,10 +236,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) continue;
             tc::fence_after_sync();
-            uint32_t v[2][32];
+            uint32_t v[2][32];                           // rows q * 32 .. + 15 and + 16 .. + 31
             const uint32_t tad = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::BN + cg);
-            tc::tmem_ld32_nw(tad, v[0]);
-            tc::tmem_ld32_nw(tad + 32, v[1]);
+            tc::tmem_ld_16x64_nw(tad, v[0]);
+            tc::tmem_ld_16x64_nw(tad + (16u << 16), v[1]);
             tc::tmem_wait_ld();
             tc::fence_before_sync();
             __syncwarp();
@@ -248,33 +250,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 if (TMA_OUT && lane == 0)                // the store before has read the staging
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
+                // blocks of 8 columns: this lane has two of them, of rows lane / 4 + 0, 8, 16, 24 (so that it
+                // needs the scales of 16 channels and not of 64)
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {         // 16 bytes of this thread's row
-                    float o[E];
+                for (int i = c0 / 8; i < (c0 + COLS) / 8; ++i) {
+                    const int c = cg + i * 8 + (lane & 3) * 2;
+                    const float2 sb = *reinterpret_cast<const float2 *>(&s_scale[b][c]);
+                    const float2 bb = BIAS ? *reinterpret_cast<const float2 *>(&s_bias[b][c]) : make_float2(0.f, 0.f);
+                    uint32_t w[4];
 #pragma unroll
-                    for (int j = 0; j < E; j += 4) {
-                        const int c = c0 + ch * E + j;
-                        const float4 s4 = *reinterpret_cast<const float4 *>(&s_scale[b][cg + c]);
-                        const float4 b4 = *reinterpret_cast<const float4 *>(&s_bias[b][cg + c]);
-                        const uint32_t *x = &v[c >> 5][c & 31];
-                        const float2 lo = fma2(mul2(make_float2((float)(int)x[0], (float)(int)x[1]), as2),
-                                               make_float2(s4.x, s4.y), make_float2(b4.x, b4.y));
-                        const float2 hi = fma2(mul2(make_float2((float)(int)x[2], (float)(int)x[3]), as2),
-                                               make_float2(s4.z, s4.w), make_float2(b4.z, b4.w));
-                        o[j] = lo.x, o[j + 1] = lo.y, o[j + 2] = hi.x, o[j + 3] = hi.y;
+                    for (int h = 0; h < 4; ++h) {
+                        const uint32_t *x = &v[h >> 1][i * 4 + (h & 1) * 2];
+                        float2 o = mul2(make_float2((float)(int)x[0], (float)(int)x[1]), make_float2(ra[h], ra[h]));
+                        o = BIAS ? fma2(o, sb, bb) : mul2(o, sb);
+                        if constexpr (BF16) {
+                            const __nv_bfloat162 z = __floats2bfloat162_rn(o.x, o.y);
+                            w[h] = *reinterpret_cast<const uint32_t *>(&z);
+                        } else {
+                            const int r = (lane >> 2) + h * 8, ch = (i & 1) * 2 + ((lane & 3) >> 1);
+                            *reinterpret_cast<float2 *>(slab + r * 64 + ((ch ^ ((r >> 1) & 3)) * 16) + (lane & 1) * 8) = o;
+                        }
                     }
-                    uint4 w;
-                    if constexpr (BF16) {
-                        const __nv_bfloat162 h0 = __floats2bfloat162_rn(o[0], o[1]), h1 = __floats2bfloat162_rn(o[2], o[3]);
-                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[4], o[5]), h3 = __floats2bfloat162_rn(o[6], o[7]);
-                        w = make_uint4(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1),
-                                       *reinterpret_cast<const uint32_t *>(&h2), *reinterpret_cast<const uint32_t *>(&h3));
-                    } else {
-                        w = make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
-                                       __float_as_uint(o[3]));
-                    }
-                    // 64-byte swizzle: chunk c of row r at c ^ (r / 2 % 4)
-                    *reinterpret_cast<uint4 *>(slab + lane * 64 + ((ch ^ ((lane >> 1) & 3)) * 16)) = w;
+                    // 64-byte swizzle: chunk c of row r at c ^ (r / 2 % 4); here lane l's is row l of chunk i
+                    if constexpr (BF16)
+                        tc::stmatrix4(tc::smem_u32(slab) + lane * 64 + (((i & 3) ^ ((lane >> 1) & 3)) * 16), w[0], w[1],
+                                      w[2], w[3]);
                 }
                 if (n0 + c0 < p.N) {
                     if (TMA_OUT) {
@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(128)
     __shared__ uint64_t full[C::NS], empty[C::NS], done;
     __shared__ uint32_t tmem_base;
     __shared__ int s_ok;
+    __shared__ float s_as[BT];                           // the tokens' scales
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (tc::smem_u32(smraw) + 1023u) & ~1023u;
     int *const part = reinterpret_cast<int *>(smraw + (base - tc::smem_u32(smraw)));
@@ -388,51 +389,66 @@ __global__ void __launch_bounds__(128)
         tc::mbar_init(&done, 1);
         tc::fence_mbar_init();
         s_ok = 1;
+        if (p.K) {
+            tc::tma_prefetch_desc(&tw);
+            tc::tma_prefetch_desc(&tx);
+        }
     }
+    const int rows = min(BT, p.M - m0);
+    if (tid < rows) s_as[tid] = p.as[m0 + tid];
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tbase = tmem_base;
 
-    if (tid == 0) {
-        // one thread loads ahead and issues the MMAs
-        constexpr uint32_t idesc = tc::idesc_i8(128, BT);
-        auto load = [&](int k) {
-            const int s = (k - k0) % C::NS;
-            const uint32_t sw = base + s * C::STAGE;
-            tc::mbar_arrive_expect_tx(&full[s], C::STAGE);
-            tc::tma_load_2d(sw, &tw, &full[s], k * 128, n0);
-            tc::tma_load_2d(sw + C::W, &tx, &full[s], k * 128, m0);
-        };
-        int issued = k0;
-        for (; issued < k1 && issued < k0 + C::NS; ++issued) load(issued);
+    if (warp == 0) {
+        // warp 0 loads, warp 1 issues the MMAs: whole warps, one elected lane acting (see wide_kernel)
+        const bool issuer = tc::elect_one();
         bool ok = true;
+        int s = 0;
+        uint32_t ph = 1;
         for (int k = k0; k < k1; ++k) {
-            const int c = k - k0, s = c % C::NS;
-            if (!(ok = tc::mbar_wait(&full[s], (uint32_t)(c / C::NS) & 1u, p.st))) break;
-            tc::fence_after_sync();
-            const uint32_t sw = base + s * C::STAGE;
-            mma_stage(tbase, sw, sw + C::W, idesc, p.K - k * 128, c == 0);
-            tc::mma_commit(&empty[s]);
-            // refill the stage of the step before, whose MMAs run ahead of these
-            if (c >= 1 && issued < k1) {
-                const int s1 = (c - 1) % C::NS;
-                if (!(ok = tc::mbar_wait(&empty[s1], (uint32_t)((c - 1) / C::NS) & 1u, p.st))) break;
-                load(issued++);
+            if (k - k0 >= C::NS) ok = tc::mbar_wait(&empty[s], ph, p.st);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (issuer) {
+                const uint32_t sw = base + s * C::STAGE;
+                tc::mbar_arrive_expect_tx(&full[s], C::STAGE);
+                tc::tma_load_2d(sw, &tw, &full[s], k * 128, n0);
+                tc::tma_load_2d(sw + C::W, &tx, &full[s], k * 128, m0);
             }
+            __syncwarp();
+            if (++s == C::NS) s = 0, ph ^= 1;
         }
-        tc::mma_commit(&done);
-        ok &= tc::mbar_wait(&done, 0, p.st);
         if (!ok) {
-            // copies issued but not consumed land before the shared memory is reused
-            for (int k = max(k0, issued - C::NS); k < issued; ++k)
-                tc::mbar_wait(&full[(k - k0) % C::NS], (uint32_t)((k - k0) / C::NS) & 1u, p.st);
+            // after a timeout: every stage's last copies land before the shared memory is reused
+            for (int k = 0; k < C::NS; ++k) tc::mbar_wait(&full[k], k < s ? ph ^ 1 : ph, p.st);
             s_ok = 0;
         }
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = tc::idesc_i8(128, BT);
+        const bool issuer = tc::elect_one();
+        bool ok = true;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int k = k0; k < k1; ++k) {
+            ok = tc::mbar_wait(&full[s], ph, p.st);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc::fence_after_sync();
+            const uint32_t sw = base + s * C::STAGE;
+            if (issuer) {
+                mma_stage(tbase, sw, sw + C::W, idesc, p.K - k * 128, k == k0);
+                tc::mma_commit(&empty[s]);
+            }
+            __syncwarp();
+            if (++s == C::NS) s = 0, ph ^= 1;
+        }
+        if (issuer) tc::mma_commit(&done);
+        __syncwarp();
+        ok &= tc::mbar_wait(&done, 0, p.st);
+        if (!__all_sync(0xffffffffu, ok)) s_ok = 0;
     }
     __syncthreads();
     tc::fence_after_sync();
-    const int rows = min(BT, p.M - m0);
     const bool ok = s_ok != 0;
     auto put = [&](int m, int n, int sum, float as, float bs, float bias) {
         const float v = fmaf((float)sum * as, bs, bias);
@@ -449,7 +465,7 @@ __global__ void __launch_bounds__(128)
             tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                if (c0 + j < rows && n < p.N) put(c0 + j, n, p.K ? (int)v[j] : 0, p.as[m0 + c0 + j], bs, bias);
+                if (c0 + j < rows && n < p.N) put(c0 + j, n, p.K ? (int)v[j] : 0, s_as[c0 + j], bs, bias);
         }
     } else {
         for (int c0 = 0; c0 < rows; c0 += 16) {
@@ -467,7 +483,7 @@ __global__ void __launch_bounds__(128)
             bias[j] = n + j < p.N ? bias_at(p, n + j) : 0.f;
         }
         auto put4 = [&](int m, const int4 &t) {
-            const float as = p.as[m0 + m];
+            const float as = s_as[m];
             const int s[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -496,7 +512,10 @@ dbc_status launch_split(const int8_t *a, int64_t lda, const int8_t *b, int64_t l
         return DBC_ERR_CUDA;
     const int nt = (p.N + 127) / 128, mt = (p.M + BT - 1) / BT, ks = (p.K + 127) / 128;
     int splits = 1;
-    while (splits < 8 && splits * 4 <= ks && (int64_t)nt * mt * splits * 2 <= 296) splits *= 2;
+    // At least two steps of depth to a CTA, and no more CTAs than run at once: one to an SM with 128
+    // tokens' stages (128 x 4096 x 4096: 12 us with four splits, 25 with eight), else two (64 x 8192 x 8192:
+    // 15.6 us with two to an SM, 22.3 with one).
+    while (splits < 8 && splits * 4 <= ks && (int64_t)nt * mt * splits * 2 <= 148 * (BT > 64 ? 1 : 2)) splits *= 2;
     if (cudaFuncSetAttribute(split_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) !=
         cudaSuccess)
         return DBC_ERR_CUDA;
@@ -524,8 +543,12 @@ dbc_status launch_wide(const int8_t *a, int64_t lda, const int8_t *b, int64_t ld
     const int64_t esz = p.out_bf16 ? 2 : 4;
     const bool tma_out = aligned16(p.out) && p.ldo * esz % 16 == 0 &&
                          tma::encode_out_rows(&to, p.out, p.out_bf16, p.M, p.N, p.ldo, 32);
-    auto *k = tma_out ? (p.out_bf16 ? wide_kernel<true, true> : wide_kernel<true, false>)
-                      : (p.out_bf16 ? wide_kernel<false, true> : wide_kernel<false, false>);
+    using K = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Args);
+    static const K kernels[8] = {wide_kernel<false, false, false>, wide_kernel<false, false, true>,
+                                 wide_kernel<false, true, false>,  wide_kernel<false, true, true>,
+                                 wide_kernel<true, false, false>,  wide_kernel<true, false, true>,
+                                 wide_kernel<true, true, false>,   wide_kernel<true, true, true>};
+    const K k = kernels[(tma_out ? 4 : 0) + (p.out_bf16 ? 2 : 0) + (p.bias ? 1 : 0)];
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
         return DBC_ERR_CUDA;
     const int64_t tiles = (int64_t)((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
@@ -559,9 +582,11 @@ extern "C" dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_sca
     const mi::Args p{a_scale, b_scale, bias, out, ldo, (int)M, (int)N, (int)K, bias_dtype == DBC_BF16,
                      out_dtype == DBC_BF16, dev_status};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    // 24 of the 74 pairs' tiles are where the wide kernel overtakes the split one (4096 x 512 x 512, 32
+    // tiles: 11.1 us against 14.2; 1000 x 1000 x 1000, 16 tiles: 13.7 against 11.5).
     const int64_t wide_tiles = ((M + 255) / 256) * ((N + 255) / 256);
     dbc_status c;
-    if (K > 0 && M > 128 && wide_tiles >= 37) c = mi::launch_wide(a, lda, b, ldb, p, st);
+    if (K > 0 && M > 128 && wide_tiles >= 24) c = mi::launch_wide(a, lda, b, ldb, p, st);
     else if (M <= 16) c = mi::launch_split<16>(a, lda, b, ldb, p, st);
     else if (M <= 32) c = mi::launch_split<32>(a, lda, b, ldb, p, st);
     else if (M <= 64) c = mi::launch_split<64>(a, lda, b, ldb, p, st);
