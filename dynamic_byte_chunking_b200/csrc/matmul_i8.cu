@@ -68,13 +68,20 @@ struct Tile {
 };
 // Tiles in groups of 16 column blocks, rows outermost inside a group: the CTAs
 // that run together share their rows of a and a group's rows of b in L2.
-__device__ __forceinline__ Tile tile_at(int64_t i, int mt, int nt) {
-    const int64_t full = (int64_t)mt * 16;
-    const int g = (int)(i / full);
-    const int64_t rem = i - g * full;
-    const int w = min(16, nt - g * 16);
-    return {(int)(rem / w), g * 16 + (int)(rem % w)};
-}
+// Divisions by a group's width go by its reciprocal (exact: fewer than 2^28
+// tiles to a group of at most 16 columns); as divisions they were a quarter of
+// the epilogue's time.
+struct Tiles {
+    uint32_t full, last, inv16, inv_last, groups;        // tiles of a full group; the last group's width
+    __device__ __forceinline__ Tiles(uint32_t mt, uint32_t nt)
+        : full(mt * 16), last((nt - 1) % 16 + 1), inv16(1u << 28), inv_last(0xffffffffu / last + 1), groups((nt + 15) / 16) {}
+    __device__ __forceinline__ Tile at(uint32_t i) const {
+        const uint32_t g = groups == 1 ? 0 : i / full, rem = i - g * full;
+        const bool tail = g + 1 == groups;
+        const uint32_t w = tail ? last : 16, m = w == 1 ? rem : __umulhi(rem, tail ? inv_last : inv16);
+        return {(int)m, (int)(g * 16 + rem - m * w)};
+    }
+};
 
 template <bool TMA_OUT, bool BF16, bool BIAS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
@@ -86,7 +93,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
     // tempty: CTA 0's, the epilogue warps of both CTAs
     __shared__ uint64_t full[C::NS], empty[C::NS], tfull[2], tempty[2], drain;
     __shared__ uint32_t tmem_base;
-    __shared__ __align__(16) float s_scale[2][C::BN], s_bias[2][C::BN];
+    __shared__ __align__(16) float s_scale[C::EPI][64], s_bias[C::EPI][64];       // each epilogue warp's channels
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = tc::cluster_rank();
     const uint32_t base = (tc::smem_u32(smraw) + 1023u) & ~1023u;
@@ -113,15 +120,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
     tc::fence_after_sync();
     const uint32_t tbase = tmem_base;
     const int mt = (p.M + C::BM - 1) / C::BM, nt = (p.N + C::BN - 1) / C::BN, ks = (p.K + 127) / 128;
-    const int64_t tiles = (int64_t)mt * nt, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int tiles = mt * nt, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const Tiles order((uint32_t)mt, (uint32_t)nt);
 
     if (warp == 0) {
         if (lane == 0) {
             int s = 0, issued = 0;                       // stage; stages in use, up to NS
             uint32_t ph = 1;                             // parity of the stage's last release
             bool ok = true;
-            for (int64_t i = pair; i < tiles && ok; i += pairs) {
-                const Tile t = tile_at(i, mt, nt);
+            for (int i = pair; i < tiles && ok; i += pairs) {
+                const Tile t = order.at(i);
                 const int y0 = t.m * C::BM + (int)rank * 128, x0 = t.n * C::BN + (int)rank * 128;
                 for (int k = 0; k < ks; ++k) {
                     if (issued == C::NS && !(ok = tc::mbar_wait(&empty[s], ph, p.st))) break;
@@ -153,9 +161,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
             const bool issuer = tc::elect_one();
             int s = 0;
             uint32_t ph = 0;
-            int64_t n = 0;
+            int n = 0;
             bool ok = true, ready = false;
-            for (int64_t i = pair; i < tiles && ok; i += pairs, ++n) {
+            for (int i = pair; i < tiles && ok; i += pairs, ++n) {
                 const int b = (int)(n & 1);
                 if (n >= 2) ok = tc::mbar_wait(&tempty[b], (uint32_t)(n / 2 - 1) & 1u, p.st);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -195,46 +203,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
         // Warp w owns TMEM lanes (w % 4) * 32 .. + 31 (its tokens) and 64 of the 256 columns.  It takes
         // them into registers at once and releases the accumulator, so that the MMAs of the tile
         // after next do not wait for the arithmetic.
-        const int q = warp & 3, cg = ((warp - 2) >> 2) * 64, et = tid - 64;
+        const int q = warp & 3, cg = ((warp - 2) >> 2) * 64;
         uint8_t *const slab = sgen + C::NS * C::STAGE + (warp - 2) * C::SLAB;
+        float *const sc = s_scale[warp - 2], *const sb = s_bias[warp - 2];
         const uint32_t release[2] = {tc::map_to(tc::smem_u32(&tempty[0]), 0), tc::map_to(tc::smem_u32(&tempty[1]), 0)};
         constexpr int COLS = BF16 ? 32 : 16;             // columns of a slab
         constexpr int E = COLS / 4;                      // elements of 16 bytes
         bool ok = true;
-        // The next tile's scales are fetched while this one is computed: a lane's four rows' by itself,
-        // the channels' scales by the first 256 threads, their bias by the others.
-        float as[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t ch_raw = 0;
-        auto fetch = [&](int64_t i) {
+        // The next tile's scales are fetched while this one is computed: a lane's four rows' and two of the
+        // warp's 64 channels', which the warp shares.  No barrier joins the warps, so that they drift apart
+        // and fill each other's waits.
+        float as[4] = {0.f, 0.f, 0.f, 0.f}, cs[2] = {0.f, 0.f};
+        uint32_t cb[2] = {0, 0};
+        Tile next = {0, 0};
+        auto fetch = [&](int i) {
             if (i >= tiles) return;
-            const Tile t = tile_at(i, mt, nt);
-            const int row = t.m * C::BM + (int)rank * 128 + q * 32 + (lane >> 2), j = t.n * C::BN + (et & 255);
+            next = order.at(i);
+            const int row = next.m * C::BM + (int)rank * 128 + q * 32 + (lane >> 2), j0 = next.n * C::BN + cg + lane;
 #pragma unroll
             for (int h = 0; h < 4; ++h)
                 if (row + h * 8 < p.M) as[h] = p.as[row + h * 8];
-            if (j < p.N) {
-                if (et < 256) ch_raw = __float_as_uint(p.bs[j]);
-                else if (BIAS && p.bias_bf16) ch_raw = static_cast<const uint16_t *>(p.bias)[j];
-                else if (BIAS) ch_raw = static_cast<const uint32_t *>(p.bias)[j];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = j0 + h * 32;
+                if (j < p.N) {
+                    cs[h] = p.bs[j];
+                    if (BIAS) cb[h] = p.bias_bf16 ? static_cast<const uint16_t *>(p.bias)[j] : static_cast<const uint32_t *>(p.bias)[j];
+                }
             }
         };
         fetch(pair);
         int b = 0;
         uint32_t ph = 0;
-        for (int64_t i = pair; i < tiles; i += pairs, ph ^= b, b ^= 1) {
-            const Tile t = tile_at(i, mt, nt);
-            const int r0 = t.m * C::BM + (int)rank * 128 + q * 32, n0 = t.n * C::BN + cg;
-            // the other buffer is still read by warps of the tile before; this one's readers are past the
-            // barrier of that tile
-            if (et < 256) s_scale[b][et] = __uint_as_float(ch_raw);
-            else if (BIAS) s_bias[b][et - 256] = __uint_as_float(p.bias_bf16 ? ch_raw << 16 : ch_raw);
+        for (int i = pair; i < tiles; i += pairs, ph ^= b, b ^= 1) {
+            const int r0 = next.m * C::BM + (int)rank * 128 + q * 32, n0 = next.n * C::BN + cg;
             const float ra[4] = {as[0], as[1], as[2], as[3]};
-            asm volatile("bar.sync 1, %0;" ::"n"(C::EPI * 32) : "memory");
+            __syncwarp();                                // the tile before has read the channels' scales
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sc[h * 32 + lane] = cs[h];
+                if (BIAS) sb[h * 32 + lane] = __uint_as_float(p.bias_bf16 ? cb[h] << 16 : cb[h]);
+            }
+            __syncwarp();
             fetch(i + pairs);
-            // after a timeout the warps still meet at the barrier above, without work
+            // (one lane polls: 32 of them slow the barriers that the MMA thread waits on)
             if (ok && lane == 0) ok = tc::mbar_wait(&tfull[b], ph, p.st);
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) continue;
+            if (!ok) break;
             tc::fence_after_sync();
             uint32_t v[2][32];                           // rows q * 32 .. + 15 and + 16 .. + 31
             const uint32_t tad = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::BN + cg);
@@ -254,15 +269,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                 // needs the scales of 16 channels and not of 64)
 #pragma unroll
                 for (int i = c0 / 8; i < (c0 + COLS) / 8; ++i) {
-                    const int c = cg + i * 8 + (lane & 3) * 2;
-                    const float2 sb = *reinterpret_cast<const float2 *>(&s_scale[b][c]);
-                    const float2 bb = BIAS ? *reinterpret_cast<const float2 *>(&s_bias[b][c]) : make_float2(0.f, 0.f);
+                    const int c = i * 8 + (lane & 3) * 2;
+                    const float2 s2 = *reinterpret_cast<const float2 *>(sc + c);
+                    const float2 b2 = BIAS ? *reinterpret_cast<const float2 *>(sb + c) : make_float2(0.f, 0.f);
                     uint32_t w[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const uint32_t *x = &v[h >> 1][i * 4 + (h & 1) * 2];
                         float2 o = mul2(make_float2((float)(int)x[0], (float)(int)x[1]), make_float2(ra[h], ra[h]));
-                        o = BIAS ? fma2(o, sb, bb) : mul2(o, sb);
+                        o = BIAS ? fma2(o, s2, b2) : mul2(o, s2);
                         if constexpr (BF16) {
                             const __nv_bfloat162 z = __floats2bfloat162_rn(o.x, o.y);
                             w[h] = *reinterpret_cast<const uint32_t *>(&z);
@@ -552,6 +567,7 @@ dbc_status launch_wide(const int8_t *a, int64_t lda, const int8_t *b, int64_t ld
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
         return DBC_ERR_CUDA;
     const int64_t tiles = (int64_t)((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
+    if (tiles > (1 << 30)) return DBC_ERR_UNSUPPORTED;   // outputs of 10^14 bytes
     k<<<(unsigned)(2 * std::min<int64_t>(tiles, num_sms() / 2)), C::THREADS, C::SMEM, st>>>(ta, tb, to, p);
     return DBC_OK;
 }
