@@ -492,7 +492,7 @@ def _elsewhere(stream, *ts):
     current first (the given one, or the tensors' device's own)."""
     torch = _torch()
     index = ts[0].get_device()
-    for t in ts:
+    for t in ts[1:]:
         if t is not None and t.get_device() != index:
             if not t.is_cuda or index < 0:
                 raise ValueError("dbc kernels take CUDA tensors only (no CPU path)")
@@ -516,10 +516,11 @@ def _here(t) -> int:
 
 
 def _like(t, dtype):
-    """A fresh contiguous tensor of t's shape."""
-    if t.dtype == dtype and t.is_contiguous():
-        return _torch().empty_like(t)
-    return t.new_empty(t.shape, dtype=dtype)
+    """A fresh contiguous tensor of t's shape (empty_like and empty_strided are the quick ways to one)."""
+    torch = _torch()
+    if t.is_contiguous():
+        return torch.empty_like(t, dtype=dtype)
+    return torch.empty(t.shape, dtype=dtype, device=t.device)
 
 
 def _code(t, what: str) -> int:
@@ -574,9 +575,10 @@ def _weight_arg(weight, d: int):
 
 
 def _width(x, what: str) -> int:
-    if x.dim() < 1 or x.shape[-1] < 1:
+    d = x.shape[-1] if x.dim() else 0
+    if d < 1:
         raise ValueError(f"{what} must be [..., d] with d >= 1")
-    return x.shape[-1]
+    return d
 
 
 def _branch(x, residual, s, d: int):
@@ -597,15 +599,18 @@ def _codes_out(x, d: int, q, scale):
     """(q [..., d] int8, its row stride, scale [...]); a fresh q has rows on 16-byte boundaries."""
     torch = _torch()
     lead = x.shape[:-1]
-    if q is None:
-        qs = (d + 15) // 16 * 16
-        q = x.new_empty((*lead, qs), dtype=torch.int8)
-        if qs != d:
-            q = q[..., :d]
-    else:
+    if q is not None:
         qs = _rows_out(q, x.shape, torch.int8, "q")
+    elif d % 16 == 0:
+        q, qs = _like(x, torch.int8), d
+    else:
+        qs = (d + 15) // 16 * 16
+        q = torch.empty((*lead, qs), dtype=torch.int8, device=x.device)[..., :d]
     if scale is None:
-        scale = x.new_empty(lead, dtype=torch.float32)
+        if len(lead) == 1:
+            scale = torch.empty_strided(lead, (1,), dtype=torch.float32, device=x.device)
+        else:
+            scale = torch.empty(lead, dtype=torch.float32, device=x.device)
     elif scale.shape != lead or scale.dtype != torch.float32 or not scale.is_contiguous():
         raise ValueError(f"scale must be a contiguous float32 tensor of shape {tuple(lead)}")
     return q, qs, scale
@@ -706,7 +711,7 @@ def rms_norm_backward(dy, s, weight=None, *, eps: float = 1e-6, dsum=None, want_
     ws = None
     if want_dw:
         if dw is None:
-            dw = s.new_empty(d, dtype=torch.float32)
+            dw = torch.empty_strided((d,), (1,), dtype=torch.float32, device=s.device)
         elif dw.shape != (d,) or dw.dtype != torch.float32 or not dw.is_contiguous():
             raise ValueError(f"dw must be a contiguous float32 tensor of shape ({d},)")
         ws = _workspace(rms_norm_backward_workspace(N, d), s.device, workspace)
@@ -765,7 +770,7 @@ def matmul_i8(a, a_scale, b, b_scale, *, bias=None, out_dtype=None, out=None, de
         bc = _code(bias, "bias")
         bias = bias.contiguous()
     if out is None:
-        out, ldo = a_scale.new_empty((M, N), dtype=out_dtype or torch.bfloat16), N
+        out, ldo = torch.empty_strided((M, N), (N, 1), dtype=out_dtype or torch.bfloat16, device=a.device), N
     else:
         ldo = _rows_out(out, (M, N), out_dtype or out.dtype, "out")
     _check("matmul_i8", lib().matmul_i8(

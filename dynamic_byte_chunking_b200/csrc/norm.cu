@@ -559,13 +559,29 @@ dbc_status launch_team(const FwdArgs &a, cudaStream_t st) {
 }
 
 // As many CTAs as are resident at once, at most `most`; 0 after a CUDA error.
+// The runtime's occupancy query costs a third of a small call's host time, so
+// each host thread remembers its last answers (they depend on the kernel and
+// the launch alone).
 constexpr int kSms = 148;
 template <class K>
 int resident(K kernel, int threads, int smem, int64_t most) {
+    struct Answer {
+        const void *kernel;
+        int threads, smem, per_sm;
+    };
+    static thread_local Answer known[8] = {};
+    static thread_local int at = 0;
+    const void *key = reinterpret_cast<const void *>(kernel);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
     int per_sm = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
-        return 0;
+    for (const Answer &k : known)
+        if (k.kernel == key && k.threads == threads && k.smem == smem) per_sm = k.per_sm;
+    if (!per_sm) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+            return 0;
+        known[at] = {key, threads, smem, per_sm};
+        at = (at + 1) % 8;
+    }
     return (int)std::min<int64_t>(most, (int64_t)per_sm * kSms);
 }
 
