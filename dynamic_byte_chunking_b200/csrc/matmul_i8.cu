@@ -595,19 +595,31 @@ extern "C" dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_sca
     if ((reinterpret_cast<uintptr_t>(out) % oa) || (bias && reinterpret_cast<uintptr_t>(bias) % ba) ||
         (reinterpret_cast<uintptr_t>(a_scale) % 4) || (reinterpret_cast<uintptr_t>(b_scale) % 4))
         return DBC_ERR_INVALID_ARG;
-    const mi::Args p{a_scale, b_scale, bias, out, ldo, (int)M, (int)N, (int)K, bias_dtype == DBC_BF16,
-                     out_dtype == DBC_BF16, dev_status};
+    mi::Args p{a_scale, b_scale, bias, out, ldo, (int)M, (int)N, (int)K, bias_dtype == DBC_BF16,
+               out_dtype == DBC_BF16, dev_status};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // 24 of the 74 pairs' tiles are where the wide kernel overtakes the split one (4096 x 512 x 512, 32
     // tiles: 11.1 us against 14.2; 1000 x 1000 x 1000, 16 tiles: 13.7 against 11.5).
     const int64_t wide_tiles = ((M + 255) / 256) * ((N + 255) / 256);
-    dbc_status c;
-    if (K > 0 && M > 128 && wide_tiles >= 24) c = mi::launch_wide(a, lda, b, ldb, p, st);
-    else if (M <= 16) c = mi::launch_split<16>(a, lda, b, ldb, p, st);
-    else if (M <= 32) c = mi::launch_split<32>(a, lda, b, ldb, p, st);
-    else if (M <= 64) c = mi::launch_split<64>(a, lda, b, ldb, p, st);
-    else c = mi::launch_split<128>(a, lda, b, ldb, p, st);
-    if (c != DBC_OK) return c;
-    count_launches(1);
+    if (K > 0 && M > 128 && wide_tiles >= 24) {
+        const dbc_status c = mi::launch_wide(a, lda, b, ldb, p, st);
+        if (c != DBC_OK) return c;
+        count_launches(1);
+        return launch_status();
+    }
+    // The split kernel's token tiles are the grid's second dimension (65535); only a depth of zero leaves
+    // it more of them than 24.
+    const int64_t most = 65535 * 128;
+    for (int64_t m0 = 0; m0 < M; m0 += most) {
+        p.M = (int)std::min<int64_t>(M - m0, most);
+        p.as = a_scale + m0;
+        p.out = static_cast<char *>(out) + m0 * ldo * (int64_t)oa;
+        const dbc_status c = M <= 16   ? mi::launch_split<16>(a, lda, b, ldb, p, st)
+                             : M <= 32 ? mi::launch_split<32>(a, lda, b, ldb, p, st)
+                             : M <= 64 ? mi::launch_split<64>(a, lda, b, ldb, p, st)
+                                       : mi::launch_split<128>(a, lda, b, ldb, p, st);
+        if (c != DBC_OK) return c;
+        count_launches(1);
+    }
     return launch_status();
 }

@@ -469,7 +469,8 @@ DBC_API dbc_status quantize_rows_i8(const void *x, int64_t x_stride, int dtype, 
  * ws       workspace of rms_norm_backward_workspace(N, d) bytes; not read when
  *          dw is NULL.  Calls that can overlap need workspaces of their own.
  * dw is summed in a fixed order: repeated calls agree bitwise.
- * Limits and errors as in rms_norm, and WORKSPACE.
+ * Limits and errors as in rms_norm, and WORKSPACE; NONFINITE is flagged for
+ * rows whose dy w or s is not finite.
  * ------------------------------------------------------------------------- */
 DBC_API size_t rms_norm_backward_workspace(int64_t N, int64_t d);
 DBC_API dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int dy_dtype, const void *s,

@@ -139,6 +139,9 @@ def test_empty_and_refused():
         out = dbc.matmul_i8(i8(M, 0), f(M), i8(300, 0), f(300), bias=bias, out_dtype=torch.float32)
         assert torch.equal(out, bias.expand(M, 300))
         assert not dbc.matmul_i8(i8(M, 0), f(M), i8(300, 0), f(300)).any()
+    rows = 65535 * 128 + 5                               # more token tiles than a grid's second dimension
+    out = dbc.matmul_i8(i8(rows, 0), f(rows), i8(2, 0), f(2), bias=bias[1:3], out_dtype=torch.float32)
+    assert torch.equal(out, bias[1:3].expand(rows, 2))
     with pytest.raises(ValueError):
         dbc.matmul_i8(i8(4, 32), f(4), i8(4, 48), f(4))
     with pytest.raises(ValueError):

@@ -412,3 +412,76 @@ def test_row_offsets_past_32_bits():
     del y, dx
     q, sc = dbc.quantize_rows_i8(x)
     assert torch.equal(q[-5:], dbc.quantize_rows_i8(tail)[0]) and torch.equal(sc[-5:], dbc.quantize_rows_i8(tail)[1])
+
+
+@pytest.mark.parametrize("T", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 200, 256, 700, 1536, 333, 1333])
+def test_codes_under_an_fp32_weight_and_near_ties(T, d):
+    """Products of more than 16 significant bits; rows whose quotients are, or are within a rounding of,
+    halves: p = (k + 1/2) m / 127 for all k, one step of fp32 up and down."""
+    import dynamic_byte_chunking_b200 as dbc
+    rng = np.random.default_rng(d)
+    N = 96
+    x = _vals(rng, (N, d), T)
+    w = _weight(rng, d, "f32")
+    q, sc, _ = dbc.rms_norm_i8(_t(x, T), _t(w, "f32"), eps=EPS)
+    qr, sr = o.rms_norm_i8(x, w, EPS)
+    assert np.array_equal(q.cpu().numpy(), qr)
+    _close(sc, sr, np.abs(sr) * (o.CHAIN / 2 + o.OPS) * o.U32, "scale")
+    if T == "f32":
+        m = rng.uniform(0.5, 2.0, (N, 1)).astype(np.float32) * np.float32(2.0) ** rng.integers(-60, 60, (N, 1)).astype(np.float32)
+        k = rng.integers(-127, 127, (N, d))
+        p = ((k + 0.5) / 127.0 * m.astype(np.float64)).astype(np.float32)
+        step = rng.integers(-1, 2, (N, d))
+        p = np.where(step > 0, np.nextafter(p, np.float32(np.inf)), np.where(step < 0, np.nextafter(p, np.float32(-np.inf)), p))
+        p[:, :1] = m
+        p = p.astype(np.float64)
+        q, sc = dbc.quantize_rows_i8(_t(p, T))
+        assert np.array_equal(q.cpu().numpy(), o.quantize_rows_i8(p)[0])
+
+
+def test_stored_sums_of_all_exponent_gaps():
+    """s = bf16(fp32(x + r)) bit for bit, over random bit patterns (subnormals, opposite signs, overflow)."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for d in (256, 1536, 777):
+        bits = torch.randint(-32768, 32768, (2, 2000, d), generator=g, device="cuda", dtype=torch.int32).to(torch.int16)
+        x, r = bits.view(torch.bfloat16)
+        x, r = torch.where(x.isfinite(), x, 1.0), torch.where(r.isfinite(), r, -1.0)
+        # half of the pairs close to each other in size
+        r = torch.where(torch.rand(r.shape, generator=g, device="cuda") < 0.5, (x.float() * 1.37).clamp(-3e38, 3e38).bfloat16().neg(), r)
+        _, s = dbc.rms_norm(x, residual=r)
+        ref = (x.float() + r.float()).bfloat16()
+        same = (s.view(torch.int16) == ref.view(torch.int16)) | (s.isnan() & ref.isnan())
+        assert bool(same.all())
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """No call needs one before it outside a capture (a child process: its first calls are captured)."""
+    import subprocess
+    import sys
+    import os
+    code = """
+import sys
+sys.path.insert(0, ROOT)
+import torch, dynamic_byte_chunking_b200 as dbc
+x = torch.randn(300, 512, device='cuda').bfloat16(); z = torch.randn(300, 99, device='cuda').bfloat16()
+st = torch.zeros(1, dtype=torch.int32, device='cuda')
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q, sc, s = dbc.rms_norm_i8(x, residual=x, dev_status=st)
+    y, _ = dbc.rms_norm(z, dev_status=st)
+    dx, dw = dbc.rms_norm_backward(x, s, dev_status=st)
+    o1 = dbc.matmul_i8(q, sc, q[:40], sc[:40], out_dtype=torch.float32, dev_status=st)
+    o2 = dbc.matmul_i8(q[:3], sc[:3], q, sc, dev_status=st)
+g.replay()
+torch.cuda.synchronize()
+assert st.item() == 0
+ref = (q.double() @ q[:40].double().t()) * sc.double()[:, None] * sc[:40].double()
+assert torch.allclose(o1.double(), ref, rtol=1e-6)
+assert torch.equal(y, dbc.rms_norm(z)[0]) and torch.equal(dx, dbc.rms_norm_backward(x, s)[0])
+print('fine')
+""".replace("ROOT", repr(os.path.dirname(os.path.dirname(os.path.abspath(__file__)))))
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and p.stdout.strip().endswith("fine"), p.stderr[-2000:]
