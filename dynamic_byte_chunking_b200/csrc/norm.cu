@@ -60,7 +60,7 @@ constexpr int block_stages(int B, int MAXT) {
 
 // R rows per team of W lanes, NV fragments per lane and row.
 template <class T, int NE, int MODE, bool RES, int W, int NV, int R>
-__global__ void __launch_bounds__(kThreads, 4) team_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, weighs(MODE) ? 4 : 1) team_kernel(const FwdArgs a) {
     const int64_t team = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / W;
     const int t = threadIdx.x % W;
     if ((((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) / W) * R >= a.N) return;   // a whole warp
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 4) team_kernel(const FwdArgs a) {
         }
         const float ss = norms(MODE) ? team_reduce<W>(s2.x + s2.y, Add()) : 1.f;
         if (MODE != kPlain) m = team_reduce<W>(m, AbsMax());
-        RowFactor k(ss, a.d, a.eps);
+        RowFactor k(ss, a);
         if (norms(MODE) && __any_sync(0xffffffffu, !(ss >= kLow && ss <= kHigh))) {
             double t2 = 0;
 #pragma unroll
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 4) team_kernel(const FwdArgs a) {
 #pragma unroll
                 for (int e = 0; e < NE; ++e) t2 += (double)f[i][j].at(e) * f[i][j].at(e);
             t2 = team_reduce<W>(t2, Add());
-            if (!(ss >= kLow && ss <= kHigh)) k = RowFactor(t2, a.d, a.eps);   // not the warp's other rows
+            if (!(ss >= kLow && ss <= kHigh)) k = RowFactor(t2, a);   // not the warp's other rows
             if (!isfinite(t2)) {
                 m = __int_as_float(0x7fc00000);
                 if (t == 0) flag(a.st, DBC_ERR_NONFINITE);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(MAXT) block_kernel(const FwdArgs a) {
         const float2 v = lane < warps ? part[ph][lane] : make_float2(0.f, 0.f);
         if (norms(MODE)) ss = team_reduce<32>(v.x, Add());
         if (MODE != kPlain) m = team_reduce<32>(v.y, AbsMax());
-        RowFactor k(ss, a.d, a.eps);
+        RowFactor k(ss, a);
         if (norms(MODE) && !(ss >= kLow && ss <= kHigh)) {     // the same in every thread
             double t2 = 0;
 #pragma unroll
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(MAXT) block_kernel(const FwdArgs a) {
             if (lane == 0) wide[warp] = t2;
             __syncthreads();
             t2 = team_reduce<32>(lane < warps ? wide[lane] : 0.0, Add());
-            k = RowFactor(t2, a.d, a.eps);
+            k = RowFactor(t2, a);
             if (!isfinite(t2)) {
                 m = __int_as_float(0x7fc00000);
                 if (t == 0) flag(a.st, DBC_ERR_NONFINITE);
@@ -268,22 +268,35 @@ struct Ring {
     static constexpr int UY = NE * (int)sizeof(TY), U = NE * (int)sizeof(T), kS = NV * UY, kDs = kS + NV * U;
     static constexpr int B = kDs + NV * U, S = block_stages(B, MAXT);
     static constexpr int smem(int threads) { return S * B * threads; }
-    // Starts the copies of row r (nothing, but still a group, when r is past the end).
-    static __device__ __forceinline__ void start(const BwdArgs &a, uint32_t base, int stage, int64_t r, int t, int W,
+    // Where the next row to copy lies; advanced by `step` rows at a time (pointers, not products of rows
+    // and strides: three of those a row were a tenth of the instructions).
+    struct Walk {
+        const TY *y;
+        const T *s, *ds;
+        int64_t left, step, dy, dss, dds;
+        __device__ __forceinline__ Walk(const BwdArgs &a, int64_t r, int64_t step_)
+            : y(static_cast<const TY *>(a.dy) + r * a.ys), s(static_cast<const T *>(a.s) + r * a.ss),
+              ds(a.ds ? static_cast<const T *>(a.ds) + r * a.ds_s : nullptr), left(a.N - r), step(step_),
+              dy(step_ * a.ys), dss(step_ * a.ss), dds(step_ * a.ds_s) {}
+    };
+    // Starts the copies of that row (nothing, but still a group, when it is past the end).
+    static __device__ __forceinline__ void start(const BwdArgs &a, Walk &k, uint32_t base, int stage, int t, int W,
                                                  int threads) {
         const uint32_t st = base + stage * B * threads;
-        const bool row = r < a.N;
-        const int64_t rr = row ? r : 0;
+        const bool row = k.left > 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (j * W + t) * NE;
             const bool in = row && col < a.d;
-            const int c = in ? col : 0;
-            ring_copy<NE>(st, j * UY, threads, static_cast<const TY *>(a.dy) + rr * a.ys + c, in);
-            ring_copy<NE>(st, kS + j * U, threads, static_cast<const T *>(a.s) + rr * a.ss + c, in);
-            if (a.ds) ring_copy<NE>(st, kDs + j * U, threads, static_cast<const T *>(a.ds) + rr * a.ds_s + c, in);
+            ring_copy<NE>(st, j * UY, threads, in ? k.y + col : static_cast<const TY *>(a.dy), in);
+            ring_copy<NE>(st, kS + j * U, threads, in ? k.s + col : static_cast<const T *>(a.s), in);
+            if (a.ds) ring_copy<NE>(st, kDs + j * U, threads, in ? k.ds + col : static_cast<const T *>(a.ds), in);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        k.y += k.dy;
+        k.s += k.dss;
+        if (a.ds) k.ds += k.dds;
+        k.left -= k.step;
     }
     static __device__ __forceinline__ void wait() { ring_wait<S>(); }
     // Fragment j of the row's dy and s; then of its ds.
@@ -321,9 +334,9 @@ __device__ __forceinline__ void bwd_stats_wide(const Frag<TY, NE> &y, const Frag
     }
 }
 template <class Q, bool DW, class TY, class T, int NE>
-__device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int stage, int64_t r, int j, int col,
-                                         int threads, const Frag<TY, NE> &y, const Frag<T, NE> &f,
-                                         const float (&w)[NE], const BwdFactor &k, float (&acc)[NE]) {
+__device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int stage, T *dx, int j, int threads,
+                                         const Frag<TY, NE> &y, const Frag<T, NE> &f, const float (&w)[NE],
+                                         const BwdFactor &k, float (&acc)[NE]) {
     float o[NE];
     const bool scaled = k.k.pre != 1.f;
 #pragma unroll
@@ -349,7 +362,7 @@ __device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int
         }
     }
     q.set(o);
-    q.store(static_cast<T *>(a.dx) + r * a.xs + col);
+    q.store(dx);
 }
 
 // Teams of W lanes walk the rows; a lane keeps the dw sums of its own columns
@@ -371,11 +384,14 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
     }
     // all teams of a warp take the same number of steps: the first team's row decides
     const int64_t first = (int64_t)blockIdx.x * (kThreads / W) + (threadIdx.x & ~31) / W, mine = lane / W;
-    for (int k = 0; k < Q::S - 1; ++k) Q::start(a, base, k, first + k * step + mine, t, W, kThreads);
+    typename Q::Walk walk(a, first + mine, step);
+    T *px = static_cast<T *>(a.dx) + (first + mine) * a.xs;
+    const int64_t dpx = step * a.xs;
+    for (int k = 0; k < Q::S - 1; ++k) Q::start(a, walk, base, k, t, W, kThreads);
     int stage = 0;
-    for (int64_t rw = first; rw < a.N; rw += step) {
+    for (int64_t rw = first; rw < a.N; rw += step, px += dpx) {
         const int64_t r = rw + mine;
-        Q::start(a, base, stage == 0 ? Q::S - 1 : stage - 1, r + (Q::S - 1) * step, t, W, kThreads);
+        Q::start(a, walk, base, stage == 0 ? Q::S - 1 : stage - 1, t, W, kThreads);
         Q::wait();
         Frag<TY, NE> y[NV];
         Frag<T, NE> f[NV];
@@ -385,21 +401,21 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], pss, psg);
         const float ss = team_reduce<W>(pss.x + pss.y, Add()), sg = team_reduce<W>(psg.x + psg.y, Add());
-        BwdFactor k(ss, sg, a.d, a.eps);
+        BwdFactor k(ss, sg, a);
         if (__any_sync(0xffffffffu, !in_range(ss, sg))) {
             double s2 = 0, g2 = 0;
 #pragma unroll
             for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
             s2 = team_reduce<W>(s2, Add());
             g2 = team_reduce<W>(g2, Add());
-            if (!in_range(ss, sg)) k = BwdFactor(s2, g2, a.d, a.eps);   // not the warp's other rows
+            if (!in_range(ss, sg)) k = BwdFactor(s2, g2, a);   // not the warp's other rows
             if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (j * W + t) * NE;
             if (r < a.N && col < a.d)
-                bwd_frag<Q, DW>(a, smem, stage, r, j, col, kThreads, y[j], f[j], w[j], k, acc[j]);
+                bwd_frag<Q, DW>(a, smem, stage, px + col, j, kThreads, y[j], f[j], w[j], k, acc[j]);
         }
         if (++stage == Q::S) stage = 0;
     }
@@ -446,10 +462,13 @@ __global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
         for (int i = 0; i < NE; ++i) w[j][i] = 1.f, acc[j][i] = 0.f;
         if (col < a.d) a.w.get<NE>(col, w[j]);
     }
-    for (int k = 0; k < Q::S - 1; ++k) Q::start(a, base, k, blockIdx.x + (int64_t)k * gridDim.x, t, W, W);
+    typename Q::Walk walk(a, blockIdx.x, gridDim.x);
+    T *px = static_cast<T *>(a.dx) + (int64_t)blockIdx.x * a.xs;
+    const int64_t dpx = (int64_t)gridDim.x * a.xs;
+    for (int k = 0; k < Q::S - 1; ++k) Q::start(a, walk, base, k, t, W, W);
     int ph = 0, stage = 0;
-    for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, ph ^= 1) {
-        Q::start(a, base, stage == 0 ? Q::S - 1 : stage - 1, r + (int64_t)(Q::S - 1) * gridDim.x, t, W, W);
+    for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, ph ^= 1, px += dpx) {
+        Q::start(a, walk, base, stage == 0 ? Q::S - 1 : stage - 1, t, W, W);
         Q::wait();
         Frag<TY, NE> y[NV];
         Frag<T, NE> f[NV];
@@ -464,7 +483,7 @@ __global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
         const float2 v = lane < warps ? part[ph][lane] : make_float2(0.f, 0.f);
         ss = team_reduce<32>(v.x, Add());
         sg = team_reduce<32>(v.y, Add());
-        BwdFactor k(ss, sg, a.d, a.eps);
+        BwdFactor k(ss, sg, a);
         if (!in_range(ss, sg)) {     // the same in every thread
             double s2 = 0, g2 = 0;
 #pragma unroll
@@ -476,13 +495,13 @@ __global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
             const double2 v2 = lane < warps ? wide[lane] : make_double2(0, 0);
             s2 = team_reduce<32>(v2.x, Add());
             g2 = team_reduce<32>(v2.y, Add());
-            k = BwdFactor(s2, g2, a.d, a.eps);
+            k = BwdFactor(s2, g2, a);
             if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (j * W + t) * NE;
-            if (col < a.d) bwd_frag<Q, DW>(a, smem, stage, r, j, col, W, y[j], f[j], w[j], k, acc[j]);
+            if (col < a.d) bwd_frag<Q, DW>(a, smem, stage, px + col, j, W, y[j], f[j], w[j], k, acc[j]);
         }
         if (++stage == Q::S) stage = 0;
     }
@@ -788,7 +807,7 @@ extern "C" dbc_status rms_norm(const void *x, int64_t x_stride, int dtype, const
                                dbc_stream_t stream) {
     DBC_NVTX_RANGE("rms_norm");
     nm::FwdArgs a{x, residual, s, y, nullptr, nullptr, {weight, w_dtype == DBC_BF16}, x_stride, r_stride, s_stride,
-                  y_stride, 0, N, (int)d, y_dtype == DBC_BF16, eps, dev_status};
+                  y_stride, 0, N, (int)d, y_dtype == DBC_BF16, eps, 1.f / (float)d, dev_status};
     const dbc_status c = nm::check_fwd(a, dtype, w_dtype, d, true);
     if (c != DBC_OK) return c;
     if (!nm::known(y_dtype)) return DBC_ERR_UNSUPPORTED;
@@ -804,7 +823,7 @@ extern "C" dbc_status rms_norm_i8(const void *x, int64_t x_stride, int dtype, co
                                   dbc_stream_t stream) {
     DBC_NVTX_RANGE("rms_norm_i8");
     nm::FwdArgs a{x, residual, s, nullptr, q, scale, {weight, w_dtype == DBC_BF16}, x_stride, r_stride, s_stride,
-                  0, q_stride, N, (int)d, 0, eps, dev_status};
+                  0, q_stride, N, (int)d, 0, eps, 1.f / (float)d, dev_status};
     const dbc_status c = nm::check_fwd(a, dtype, w_dtype, d, true);
     if (c != DBC_OK) return c;
     if (q_stride < d) return DBC_ERR_INVALID_ARG;
@@ -817,7 +836,7 @@ extern "C" dbc_status quantize_rows_i8(const void *x, int64_t x_stride, int dtyp
                                        int64_t q_stride, float *scale, int32_t *dev_status, dbc_stream_t stream) {
     DBC_NVTX_RANGE("quantize_rows_i8");
     nm::FwdArgs a{x, nullptr, nullptr, nullptr, q, scale, {nullptr, 0}, x_stride, 0, 0, 0, q_stride, N, (int)d, 0,
-                  1.f, dev_status};
+                  1.f, 1.f, dev_status};
     const dbc_status c = nm::check_fwd(a, dtype, DBC_F32, d, false);
     if (c != DBC_OK) return c;
     if (q_stride < d) return DBC_ERR_INVALID_ARG;
@@ -854,7 +873,7 @@ extern "C" dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int d
     if (dw && (!ws || !nm::aligned_to(ws, 16) || ws_bytes < rms_norm_backward_workspace(N, d)))
         return DBC_ERR_WORKSPACE;
     const nm::BwdArgs a{dy, s, ds, dx, {weight, w_dtype == DBC_BF16}, dy_stride, s_stride, ds_stride, dx_stride, N,
-                        (int)d, eps, dw ? static_cast<float *>(ws) : nullptr, dev_status};
+                        (int)d, eps, 1.f / (float)d, dw ? static_cast<float *>(ws) : nullptr, dev_status};
     using B = __nv_bfloat16;
     const bool by = dy_dtype == DBC_BF16, bs = dtype == DBC_BF16;
     const int lines = by && bs ? nm::launch_bwd<B, B>(a, st)

@@ -335,7 +335,7 @@ struct FwdArgs {
     Weight w;
     int64_t xs, rs, ss, ys, qs, N;
     int d, y_bf16;
-    float eps;
+    float eps, inv_d;
     int32_t *st;
 };
 
@@ -343,11 +343,13 @@ struct FwdArgs {
 // is 1 unless rstd would be subnormal) and the 8-bit scale.
 struct RowFactor {
     float pre, rstd;
-    __device__ __forceinline__ RowFactor(float ss, int d, float eps) : pre(1.f) {
-        rstd = rsqrtf(ss / (float)d + eps);
+    template <class A>
+    __device__ __forceinline__ RowFactor(float ss, const A &a) : pre(1.f) {
+        rstd = rsqrtf(fmaf(ss, a.inv_d, a.eps));
     }
-    __device__ __forceinline__ RowFactor(double ss, int d, float eps) {
-        const double r = 1.0 / sqrt(ss / d + (double)eps);
+    template <class A>
+    __device__ __forceinline__ RowFactor(double ss, const A &a) {
+        const double r = 1.0 / sqrt(ss / a.d + (double)a.eps);
         pre = r < 0x1p-120 ? 0x1p-16f : 1.f;
         rstd = (float)(r / (double)pre);
     }
@@ -368,7 +370,7 @@ struct BwdArgs {
     Weight w;
     int64_t ys, ss, ds_s, xs, N;
     int d;
-    float eps;
+    float eps, inv_d;
     float *part;                 // one line of d dw sums per CTA, or NULL
     int32_t *st;
 };
@@ -379,11 +381,11 @@ __device__ __forceinline__ bool in_range(float ss, float sg) { return ss >= kLow
 struct BwdFactor {
     RowFactor k;
     float c;
-    __device__ __forceinline__ BwdFactor(float ss, float sg, int d, float eps) : k(ss, d, eps) {
-        c = sg / (float)d * k.rstd;
+    __device__ __forceinline__ BwdFactor(float ss, float sg, const BwdArgs &a) : k(ss, a) {
+        c = sg * a.inv_d * k.rstd;
     }
-    __device__ __forceinline__ BwdFactor(double ss, double sg, int d, float eps) : k(ss, d, eps) {
-        c = (float)(sg / d * (double)k.rstd * (double)k.pre);
+    __device__ __forceinline__ BwdFactor(double ss, double sg, const BwdArgs &a) : k(ss, a) {
+        c = (float)(sg / a.d * (double)k.rstd * (double)k.pre);
     }
 };
 

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) odd_tile_kernel(const FwdArgs a, int
             }
             if (norms(MODE)) ss = team_reduce<W>(ss, Add());
             if (MODE != kPlain) m = team_reduce<W>(m, AbsMax());
-            RowFactor f(ss, a.d, a.eps);
+            RowFactor f(ss, a);
             const bool odd = norms(MODE) && live && !(ss >= kLow && ss <= kHigh);
             if (norms(MODE) && __any_sync(0xffffffffu, odd)) {
                 double t2 = 0;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) odd_tile_kernel(const FwdArgs a, int
                     t2 += v * v;
                 }
                 t2 = team_reduce<W>(t2, Add());
-                if (odd) f = RowFactor(t2, a.d, a.eps);
+                if (odd) f = RowFactor(t2, a);
                 if (odd && !isfinite(t2)) {
                     m = __int_as_float(0x7fc00000);
                     if (t == 0) flag(a.st, DBC_ERR_NONFINITE);
@@ -282,13 +282,13 @@ __global__ void __launch_bounds__(MAXT) odd_kernel(const FwdArgs a, int slot, in
         }
         const float2 sm = team_pair(make_float2(ss, m), Add(), AbsMax(), sh);
         ss = sm.x, m = sm.y;
-        RowFactor k(ss, a.d, a.eps);
+        RowFactor k(ss, a);
         if (norms(MODE) && !(ss >= kLow && ss <= kHigh)) {   // the same in the whole team
             double t2 = 0;
 #pragma unroll
             for (int j = 0; j < NV; ++j) t2 += (double)v[j] * v[j];
             t2 = team_pair(make_double2(t2, 0), Add(), Add(), shw).x;
-            k = RowFactor(t2, a.d, a.eps);
+            k = RowFactor(t2, a);
             if (!isfinite(t2)) {
                 m = __int_as_float(0x7fc00000);
                 if (t == 0) flag(a.st, DBC_ERR_NONFINITE);
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) odd_bwd_tile_kernel(const BwdArgs a,
             }
             ss = team_reduce<W>(ss, Add());
             sg = team_reduce<W>(sg, Add());
-            BwdFactor b(ss, sg, a.d, a.eps);
+            BwdFactor b(ss, sg, a);
             const bool odd = k < rows && !in_range(ss, sg);
             if (__any_sync(0xffffffffu, odd)) {
                 double s2 = 0, g2 = 0;
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads) odd_bwd_tile_kernel(const BwdArgs a,
                 }
                 s2 = team_reduce<W>(s2, Add());
                 g2 = team_reduce<W>(g2, Add());
-                if (odd) b = BwdFactor(s2, g2, a.d, a.eps);
+                if (odd) b = BwdFactor(s2, g2, a);
                 if (odd && t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
             }
             T *const o = tile_row(obuf, slot, X + r0 * a.xs, a.xs, k, a.d);
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(MAXT) odd_bwd_kernel(const BwdArgs a, int yslo
             p.y = fmaf(y[j] * w[j], f[j], p.y);
         }
         p = team_pair(p, Add(), Add(), sh);       // (its barrier: everybody has read s)
-        BwdFactor k(p.x, p.y, a.d, a.eps);
+        BwdFactor k(p.x, p.y, a);
         if (!in_range(p.x, p.y)) {                       // the same in the whole team
             double2 q = make_double2(0, 0);
 #pragma unroll
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(MAXT) odd_bwd_kernel(const BwdArgs a, int yslo
                 q.y += (double)(y[j] * w[j]) * f[j];
             }
             q = team_pair(q, Add(), Add(), shw);
-            k = BwdFactor(q.x, q.y, a.d, a.eps);
+            k = BwdFactor(q.x, q.y, a);
             if (t == 0 && (!isfinite(q.x) || !isfinite(q.y))) flag(a.st, DBC_ERR_NONFINITE);
         }
         T *const dx = static_cast<T *>(a.dx) + r * a.xs;
