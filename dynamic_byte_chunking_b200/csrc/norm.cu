@@ -631,10 +631,11 @@ inline OddPlan odd_plan(int d, int nv, int in_bytes, int out_bytes) {
     const int stages = 2 * in_bytes + out_bytes <= 100 * 1024 ? 2 : 1;
     return {((d + nv - 1) / nv + 31) / 32 * 32, stages, stages * in_bytes + out_bytes};
 }
-// Rows of a tile: about 8 KB of them, whole passes of the teams, and not so many
-// that SMs stay without a tile.
-inline int odd_tile_rows(int64_t N, int row_bytes, int teams) {
-    return std::max(1, (int)std::min<int64_t>(8192 / row_bytes, N / (kSms * 4)) / teams) * teams;
+// Rows of a tile: whole passes of the teams, `budget` bytes of shared memory at `row_bytes` a row, and
+// not so many that SMs stay without a tile.  Four CTAs to an SM forward (100000 x 257: 78 us with 56 KB,
+// 85 with 28, 94 with 78), two backward (92 us with 91 KB, 117 with 30).
+inline int odd_tile_rows(int64_t N, int row_bytes, int teams, int budget) {
+    return std::max(1, (int)std::min<int64_t>(budget / row_bytes, N / (kSms * 4)) / teams) * teams;
 }
 
 template <class T, int MODE, bool RES, int NV, int MAXT>
@@ -651,9 +652,9 @@ template <class T, int MODE, bool RES, int W>
 dbc_status launch_odd_tile(const FwdArgs &a, cudaStream_t st) {
     constexpr int TEAMS = kThreads / W;
     const int slot = slot_bytes(a.d, sizeof(T)), oslot = slot_bytes(a.d, MODE != kPlain ? 1 : a.y_bf16 ? 2 : 4);
-    const int R = odd_tile_rows(a.N, a.d * (int)sizeof(T), TEAMS);
     constexpr int IN = RES ? 2 : 1;
-    const int smem = R * ((2 * IN + (RES && a.s ? 1 : 0)) * slot + oslot) + a.d * 4;
+    const int row = (2 * IN + (RES && a.s ? 1 : 0)) * slot + oslot;
+    const int R = odd_tile_rows(a.N, row, TEAMS, 56 * 1024 - 4 * a.d), smem = R * row + a.d * 4;
     auto *k = odd_tile_kernel<T, MODE, RES, W>;
     const int ctas = resident(k, kThreads, smem, (a.N + R - 1) / R);
     if (!ctas) return DBC_ERR_CUDA;
@@ -742,8 +743,8 @@ int launch_odd_bwd_row(const BwdArgs &a, cudaStream_t st) {
 template <class TY, class T, int W, int NV>
 int launch_odd_bwd_tile(const BwdArgs &a, cudaStream_t st) {
     const int yslot = slot_bytes(a.d, sizeof(TY)), slot = slot_bytes(a.d, sizeof(T));
-    const int R = odd_tile_rows(a.N, a.d * (int)sizeof(T), kThreads / W);
-    const int smem = R * (2 * (yslot + (a.ds ? 2 : 1) * slot) + slot);
+    const int row = 2 * (yslot + (a.ds ? 2 : 1) * slot) + slot;
+    const int R = odd_tile_rows(a.N, row, kThreads / W, 92 * 1024), smem = R * row;
     auto *k = a.part ? odd_bwd_tile_kernel<TY, T, true, W, NV> : odd_bwd_tile_kernel<TY, T, false, W, NV>;
     const int ctas = resident(k, kThreads, smem, std::min<int64_t>(bwd_lines(a.N, a.d), (a.N + R - 1) / R));
     if (ctas) k<<<ctas, kThreads, smem, st>>>(a, R, yslot, slot);
