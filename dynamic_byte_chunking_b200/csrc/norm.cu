@@ -60,7 +60,7 @@ constexpr int block_stages(int B, int MAXT) {
 
 // R rows per team of W lanes, NV fragments per lane and row.
 template <class T, int NE, int MODE, bool RES, int W, int NV, int R>
-__global__ void __launch_bounds__(kThreads, weighs(MODE) ? 4 : 1) team_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, weighs(MODE) ? 4 : 0) team_kernel(const FwdArgs a) {
     const int64_t team = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / W;
     const int t = threadIdx.x % W;
     if ((((int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31)) / W) * R >= a.N) return;   // a whole warp

@@ -246,10 +246,10 @@ struct Quant {
         const float f = d > 0.f ? h + 0.5f : d < 0.f ? h - 0.5f : rintf(h);
         return f + kMagic;
     }
+    // Codes in the low bytes of u (anything for a bad row).
     template <bool NARROW, int NE>
-    __device__ __forceinline__ void store(int8_t *q, const float (&p_)[NE]) const {
+    __device__ __forceinline__ void codes(const float (&p_)[NE], uint32_t (&u)[NE]) const {
         constexpr float kMagic = 12582912.f;
-        uint32_t u[NE];
         float p[NE], ms = m, rs = rinv;
 #pragma unroll
         for (int i = 0; i < NE; ++i) p[i] = p_[i];
@@ -260,33 +260,28 @@ struct Quant {
 #pragma unroll
             for (int i = 0; i < NE; ++i) p[i] *= k;    // exact, or too small to matter
         }
-        if constexpr (NE == 1) {
-            const float a = 127.f * p[0], t0 = a * rs, t = fmaf(fmaf(-t0, ms, a), rs, t0);
-            u[0] = __float_as_uint(settle<NARROW>(p[0], ms, t + kMagic, t));
-        } else {
-            const float2 c127 = make_float2(127.f, 127.f), mm = make_float2(-ms, -ms), rr = make_float2(rs, rs);
+        const float2 c127 = make_float2(127.f, 127.f), mm = make_float2(-ms, -ms), rr = make_float2(rs, rs);
 #pragma unroll
-            for (int i = 0; i < NE; i += 2) {
-                const float2 a = mul2(make_float2(p[i], p[i + 1]), c127);
-                const float2 t0 = mul2(a, rr);
-                const float2 t = fma2(fma2(t0, mm, a), rr, t0);
-                const float2 v = add2(t, make_float2(kMagic, kMagic));
-                u[i] = __float_as_uint(settle<NARROW>(p[i], ms, v.x, t.x));
-                u[i + 1] = __float_as_uint(settle<NARROW>(p[i + 1], ms, v.y, t.y));
-            }
+        for (int i = 0; i < NE; i += 2) {
+            const float2 a = mul2(make_float2(p[i], p[i + 1]), c127);
+            const float2 t0 = mul2(a, rr);
+            const float2 t = fma2(fma2(t0, mm, a), rr, t0);
+            const float2 v = add2(t, make_float2(kMagic, kMagic));
+            u[i] = __float_as_uint(settle<NARROW>(p[i], ms, v.x, t.x));
+            u[i + 1] = __float_as_uint(settle<NARROW>(p[i + 1], ms, v.y, t.y));
         }
-        if constexpr (NE == 1) {
-            *q = bad ? (int8_t)0 : (int8_t)u[0];
-        } else {
-            uint32_t w[NE / 4];
+    }
+    template <bool NARROW, int NE>
+    __device__ __forceinline__ void store(int8_t *q, const float (&p)[NE]) const {
+        uint32_t u[NE], w[NE / 4];
+        codes<NARROW>(p, u);
 #pragma unroll
-            for (int i = 0; i < NE / 4; ++i)
-                w[i] = bad ? 0u
-                           : __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040),
-                                         __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040), 0x5410);
-            if constexpr (NE == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t *>(q) = w[0];
-        }
+        for (int i = 0; i < NE / 4; ++i)
+            w[i] = bad ? 0u
+                       : __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040),
+                                     __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040), 0x5410);
+        if constexpr (NE == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(q) = w[0];
     }
 };
 

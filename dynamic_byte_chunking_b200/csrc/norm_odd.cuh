@@ -205,12 +205,20 @@ __global__ void __launch_bounds__(kThreads) odd_tile_kernel(const FwdArgs a, int
                 }
             } else {
                 int8_t *const o = tile_row(obuf, oslot, a.q + r0 * a.qs, a.qs, k, a.d);
-#pragma unroll 4
-                for (int c = t; c < n; c += W) {
-                    const float v = val(c);
-                    if (RES && S) st_f(so + c, v);
-                    const float p[1] = {weighs(MODE) ? v * w[c] : v};
-                    qn.template store<narrow<T>(MODE), 1>(o + c, p);
+                // two columns at a time: loads, packed arithmetic, stores
+#pragma unroll 2
+                for (int c = t; c < n; c += 2 * W) {
+                    const bool two = c + W < n;
+                    const float v[2] = {val(c), two ? val(c + W) : 0.f};
+                    const float p[2] = {weighs(MODE) ? v[0] * w[c] : v[0], weighs(MODE) && two ? v[1] * w[c + W] : v[1]};
+                    uint32_t u[2];
+                    qn.template codes<narrow<T>(MODE)>(p, u);
+                    if (RES && S) st_f(so + c, v[0]);
+                    o[c] = qn.bad ? 0 : (int8_t)u[0];
+                    if (two) {
+                        if (RES && S) st_f(so + c + W, v[1]);
+                        o[c + W] = qn.bad ? 0 : (int8_t)u[1];
+                    }
                 }
                 if (t == 0 && live) {
                     a.scale[r0 + k] = row_scale<MODE>(qn, f);
@@ -314,11 +322,16 @@ __global__ void __launch_bounds__(MAXT) odd_kernel(const FwdArgs a, int slot, in
         } else {
             int8_t *const qo = reinterpret_cast<int8_t *>(out + off16(a.q + r * a.qs));
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (j * W + t < a.d) {
-                    const float p[1] = {weighs(MODE) ? v[j] * w[j] : v[j]};
-                    qn.template store<narrow<T>(MODE), 1>(qo + j * W + t, p);
-                }
+            for (int j = 0; j < NV; j += 4) {
+                float p[4];
+                uint32_t u[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) p[q] = weighs(MODE) ? v[j + q] * w[j + q] : v[j + q];
+                qn.template codes<narrow<T>(MODE)>(p, u);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if ((j + q) * W + t < a.d) qo[(j + q) * W + t] = qn.bad ? 0 : (int8_t)u[q];
+            }
             if (t == 0) {
                 a.scale[r] = row_scale<MODE>(qn, k);
                 if (qn.bad) flag(a.st, DBC_ERR_NONFINITE);
