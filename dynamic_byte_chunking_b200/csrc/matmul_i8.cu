@@ -15,6 +15,11 @@
 //     and not 128 lanes; the depth is split over a cluster of up to 8 CTAs,
 //     whose partial sums (integers: any order gives the same) are joined through
 //     distributed shared memory.
+// Measured (us on the device): 8192 x 4096 x 4096 94 in short runs (2.9 P op/s, 86 % of twice the
+// measured bf16 rate; the tensor pipe is fed without a pause: a stage of 512 cycles' MMAs every 541) and
+// 108 in long ones, where the power cap holds the clock near 1.45 GHz (torch._int_mm, without scales: 106);
+// 32768 x 1536 x 512 34 (outputs and their staging share the time with the loads: 28 without the stores,
+// 24 without the epilogue's arithmetic); 4 x 8192 x 8192 10.6 (98 % of HBM's copy rate).
 // Every wait is bounded; a timeout flags DBC_ERR_TIMEOUT and the CTA skips its
 // remaining work, after waiting for its copies and MMAs in flight.
 #include <cuda.h>
@@ -532,8 +537,10 @@ dbc_status launch_split(const int8_t *a, int64_t lda, const int8_t *b, int64_t l
     // 15.6 us with two to an SM, 22.3 with one).
     while (splits < 8 && splits * 4 <= ks && (int64_t)nt * mt * splits * 2 <= 148 * (BT > 64 ? 1 : 2)) splits *= 2;
     if (cudaFuncSetAttribute(split_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) !=
-        cudaSuccess)
+        cudaSuccess) {
+        cudaGetLastError();                              // not the next call's
         return DBC_ERR_CUDA;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(nt * splits), (unsigned)mt);
     cfg.blockDim = dim3(128);
@@ -545,7 +552,10 @@ dbc_status launch_split(const int8_t *a, int64_t lda, const int8_t *b, int64_t l
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, split_kernel<BT>, tw, tx, p, splits) != cudaSuccess) return DBC_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, split_kernel<BT>, tw, tx, p, splits) != cudaSuccess) {
+        cudaGetLastError();
+        return DBC_ERR_CUDA;
+    }
     return DBC_OK;
 }
 
@@ -564,8 +574,10 @@ dbc_status launch_wide(const int8_t *a, int64_t lda, const int8_t *b, int64_t ld
                                  wide_kernel<true, false, false>,  wide_kernel<true, false, true>,
                                  wide_kernel<true, true, false>,   wide_kernel<true, true, true>};
     const K k = kernels[(tma_out ? 4 : 0) + (p.out_bf16 ? 2 : 0) + (p.bias ? 1 : 0)];
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess) {
+        cudaGetLastError();                              // not the next call's
         return DBC_ERR_CUDA;
+    }
     const int64_t tiles = (int64_t)((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
     if (tiles > (1 << 30)) return DBC_ERR_UNSUPPORTED;   // outputs of 10^14 bytes
     k<<<(unsigned)(2 * std::min<int64_t>(tiles, num_sms() / 2)), C::THREADS, C::SMEM, st>>>(ta, tb, to, p);

@@ -8,9 +8,9 @@
 namespace dbc {
 namespace nm {
 
-// NE consecutive elements of a row in registers: 16 bytes (NE = 8 bf16 or 4
-// fp32), or one element (NE = 1, rows off the 16-byte grid and odd widths).
-// Rows bypass L1 (read once); what all rows share is kept there.
+// NE consecutive elements of a row in registers: 16 bytes of the row's type (8
+// bf16 or 4 fp32; 8 fp32 or 4 bf16 of an array of the other type beside it), or
+// one element.  Rows bypass L1 (read once); what all rows share is kept there.
 template <class T, int NE>
 struct Frag;
 
@@ -94,15 +94,10 @@ struct Frag<__nv_bfloat16, 4> {
 template <>
 struct Frag<__nv_bfloat16, 1> {
     __nv_bfloat16 b;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-        const uint16_t u = __ldcg(reinterpret_cast<const unsigned short *>(p));
-        b = __ushort_as_bfloat16(u);
-    }
     __device__ __forceinline__ void load_shared_by_rows(const __nv_bfloat16 *p) {
         b = __ushort_as_bfloat16(__ldg(reinterpret_cast<const unsigned short *>(p)));
     }
     __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *p = b; }
-    __device__ __forceinline__ void zero() { b = __ushort_as_bfloat16(0); }
     __device__ __forceinline__ float at(int) const { return __bfloat162float(b); }
     __device__ __forceinline__ void set(const float (&v)[1]) { b = __float2bfloat16_rn(v[0]); }
 };

@@ -407,8 +407,8 @@ DBC_API dbc_status hnet_route(const void *H, const int64_t *offsets, int64_t row
  * y        out [N, d] fp32 or bf16 (y_dtype), y_stride.  May be x itself, and
  *          residual when s is neither, given equal types and strides.  Other
  *          overlaps of inputs and outputs are not allowed.
- * All strides are in elements, >= d.  Any d from 1 to 16384; 16-byte accesses
- * when d is a multiple of 8 and every row starts on a 16-byte boundary.
+ * All strides are in elements, >= d.  Any d from 1 to 16384; quickest where
+ * every row starts on a 16-byte boundary and holds a multiple of 16 bytes.
  * A row with a NaN gives NaN, one with an infinity 0 and NaN at the infinity;
  * both flag NONFINITE.
  * Errors: INVALID_ARG (NULL/negative/stride < d/eps not finite and > 0/a

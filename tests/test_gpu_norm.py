@@ -485,3 +485,24 @@ print('fine')
 """.replace("ROOT", repr(os.path.dirname(os.path.dirname(os.path.abspath(__file__)))))
     p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert p.returncode == 0 and p.stdout.strip().endswith("fine"), p.stderr[-2000:]
+
+
+@pytest.mark.parametrize("d", [96, 256, 1000, 2048, 99, 501, 1531, 3001])
+def test_sum_that_is_not_stored(d):
+    """The library's calls with a residual and no s (the binding always stores it)."""
+    import ctypes
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    rng = np.random.default_rng(d)
+    N = 700
+    x, r, w = (_t(_vals(rng, s, "bf16"), "bf16") for s in ((N, d), (N, d), (d,)))
+    y, _ = dbc.rms_norm(x, w, residual=r)
+    q, sc, _ = dbc.rms_norm_i8(x, w, residual=r)
+    y2, q2, sc2 = torch.zeros_like(y), torch.zeros(N, d, dtype=torch.int8, device="cuda"), torch.zeros_like(sc)
+    L, st = dbc.lib(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert L.rms_norm(x.data_ptr(), d, 1, r.data_ptr(), d, w.data_ptr(), 1, N, d, 1e-6, None, 0, y2.data_ptr(), d, 1,
+                      None, st) == 0
+    assert L.rms_norm_i8(x.data_ptr(), d, 1, r.data_ptr(), d, w.data_ptr(), 1, N, d, 1e-6, None, 0, q2.data_ptr(), d,
+                         sc2.data_ptr(), None, st) == 0
+    # (q2's rows are d bytes apart, q's on 16-byte boundaries: two routes through memory, the same codes)
+    assert torch.equal(y, y2) and torch.equal(q, q2) and torch.allclose(sc, sc2, rtol=1e-6)
