@@ -16,7 +16,7 @@
 // Measured (us on the device, of a copy's time for the same bytes): 2.2 M x 256
 // bf16 with residual 684 (102 %), 262144 x 512 158 (104 %), 20000 x 4096 103
 // (98 %); the 8-bit form 154 (94 %) and 103 (86 %), where the arithmetic of the
-// codes shows (14 instructions an element); backward 100000 x 512 65 (98 %),
+// codes shows (two issue slots of three are taken); backward 100000 x 512 65 (98 %),
 // 65536 x 256 26 (81 %, with the join of the dw lines), 32749 x 1536 with fp32
 // dy 86 (73 %: its 137 registers leave an SM 12 warps; fewer registers spill
 // (153 us), fewer columns per thread pay more barriers (100 us)).
