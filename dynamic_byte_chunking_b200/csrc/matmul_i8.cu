@@ -383,6 +383,9 @@ __device__ __forceinline__ void join(uint32_t base, uint32_t rank, int rows, F p
     }
 }
 
+__device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
 template <int BT>
 __global__ void __launch_bounds__(128)
     split_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const Args p,
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(128)
         }
     }
     const int rows = min(BT, p.M - m0);
-    if (tid < rows) s_as[tid] = p.as[m0 + tid];
+    if (tid < BT) s_as[tid] = tid < rows ? p.as[m0 + tid] : 0.f;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -479,14 +482,22 @@ __global__ void __launch_bounds__(128)
     if (splits == 1) {
         const int n = n0 + tid;                         // this thread's channel
         const float bs = n < p.N ? p.bs[n] : 0.f, bias = n < p.N ? bias_at(p, n) : 0.f;
-        for (int c0 = 0; c0 < rows && ok; c0 += 16) {
-            uint32_t v[16];
-            tc::tmem_ld16_nw(tbase + ((uint32_t)(warp * 32) << 16) + c0, v);
-            tc::tmem_wait_ld();
+        auto column = [&](auto *o) {
+            o += (int64_t)m0 * p.ldo + n;
+            for (int c0 = 0; c0 < rows && ok; c0 += 16) {
+                uint32_t v[16];
+                tc::tmem_ld16_nw(tbase + ((uint32_t)(warp * 32) << 16) + c0, v);
+                tc::tmem_wait_ld();
+                float f[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (c0 + j < rows && n < p.N) put(c0 + j, n, p.K ? (int)v[j] : 0, s_as[c0 + j], bs, bias);
-        }
+                for (int j = 0; j < 16; ++j) f[j] = fmaf((p.K ? (float)(int)v[j] : 0.f) * s_as[c0 + j], bs, bias);
+#pragma unroll
+                for (int j = 0; j < 16; ++j, o += p.ldo)
+                    if (c0 + j < rows && n < p.N) store_one(o, f[j]);
+            }
+        };
+        if (p.out_bf16) column(static_cast<__nv_bfloat16 *>(p.out));
+        else column(static_cast<float *>(p.out));
     } else {
         for (int c0 = 0; c0 < rows; c0 += 16) {
             uint32_t v[16];
@@ -533,8 +544,8 @@ dbc_status launch_split(const int8_t *a, int64_t lda, const int8_t *b, int64_t l
     const int nt = (p.N + 127) / 128, mt = (p.M + BT - 1) / BT, ks = (p.K + 127) / 128;
     int splits = 1;
     // At least two steps of depth to a CTA, and no more CTAs than run at once: one to an SM with 128
-    // tokens' stages (128 x 4096 x 4096: 12 us with four splits, 25 with eight), else two (64 x 8192 x 8192:
-    // 15.6 us with two to an SM, 22.3 with one).
+    // tokens' stages (128 x 4096 x 4096 took 12 us with four splits, 25 with eight), else two (64 x 8192 x
+    // 8192 took 15.6 us with two to an SM, 22.3 with one).
     while (splits < 8 && splits * 4 <= ks && (int64_t)nt * mt * splits * 2 <= 148 * (BT > 64 ? 1 : 2)) splits *= 2;
     if (cudaFuncSetAttribute(split_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) !=
         cudaSuccess) {
@@ -611,7 +622,7 @@ extern "C" dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_sca
                out_dtype == DBC_BF16, dev_status};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // 24 of the 74 pairs' tiles are where the wide kernel overtakes the split one (4096 x 512 x 512, 32
-    // tiles: 11.1 us against 14.2; 1000 x 1000 x 1000, 16 tiles: 13.7 against 11.5).
+    // tiles: 10.8 us against 14.2; 1000 x 1000 x 1000, 16 tiles: 13.7 against 9.1).
     const int64_t wide_tiles = ((M + 255) / 256) * ((N + 255) / 256);
     if (K > 0 && M > 128 && wide_tiles >= 24) {
         const dbc_status c = mi::launch_wide(a, lda, b, ldb, p, st);
@@ -621,15 +632,20 @@ extern "C" dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_sca
     }
     // The split kernel's token tiles are the grid's second dimension (65535); only a depth of zero leaves
     // it more of them than 24.
-    const int64_t most = 65535 * 128;
+    const int64_t most = 65535 * 128, nt = (N + 127) / 128;
+    // Tokens of a tile: as few as leave at most 74 tiles, so that short epilogues run side by side
+    // (300 x 300 x 128: 3.7 us against 5.1 with 128 tokens) and long weights are not read by many tiles
+    // (64 x 8192 x 8192: 12.5 us against 15.8 with at most 148).
+    int tile = 16;
+    while (tile < 128 && tile < M && ((M + tile - 1) / tile) * nt > 74) tile *= 2;
     for (int64_t m0 = 0; m0 < M; m0 += most) {
         p.M = (int)std::min<int64_t>(M - m0, most);
         p.as = a_scale + m0;
         p.out = static_cast<char *>(out) + m0 * ldo * (int64_t)oa;
-        const dbc_status c = M <= 16   ? mi::launch_split<16>(a, lda, b, ldb, p, st)
-                             : M <= 32 ? mi::launch_split<32>(a, lda, b, ldb, p, st)
-                             : M <= 64 ? mi::launch_split<64>(a, lda, b, ldb, p, st)
-                                       : mi::launch_split<128>(a, lda, b, ldb, p, st);
+        const dbc_status c = tile <= 16   ? mi::launch_split<16>(a, lda, b, ldb, p, st)
+                             : tile <= 32 ? mi::launch_split<32>(a, lda, b, ldb, p, st)
+                             : tile <= 64 ? mi::launch_split<64>(a, lda, b, ldb, p, st)
+                                          : mi::launch_split<128>(a, lda, b, ldb, p, st);
         if (c != DBC_OK) return c;
         count_launches(1);
     }
