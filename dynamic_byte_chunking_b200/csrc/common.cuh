@@ -85,6 +85,16 @@ __device__ __forceinline__ int64_t find_row(const int64_t *offs, int64_t rows, i
     return lo;
 }
 
+// Raises a kernel's dynamic shared-memory limit to `most`, the largest size that any call launches it
+// with.  The limit belongs to the kernel and not to the calling host thread: were it set to each call's
+// own size, a thread could lower it between another's setting and its launch, which would be refused.
+template <class K>
+inline bool allow_smem(K kernel, size_t most) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess) return true;
+    cudaGetLastError();                              // not the next call's
+    return false;
+}
+
 // Names one C-ABI call in profiler timelines (an NVTX range; header-only, and
 // without an attached tool each push/pop is a call through a null hook).
 struct NvtxRange {

@@ -597,6 +597,10 @@ dbc_status launch_team(const FwdArgs &a, cudaStream_t st) {
 // each host thread remembers its last answers (they depend on the kernel and
 // the launch alone).
 constexpr int kSms = 148;
+// More dynamic shared memory than any launch here asks for (block_stages allows 200 KB; the tiles of odd rows
+// take up to 197 KB, at eight rows of 1024 fp32 elements), and with the 16 KB of static shared memory that one
+// kernel has beside it within a CTA's 227 KB.
+constexpr int kMostSmem = 208 * 1024;
 template <class K>
 int resident(K kernel, int threads, int smem, int64_t most) {
     struct Answer {
@@ -606,10 +610,7 @@ int resident(K kernel, int threads, int smem, int64_t most) {
     static thread_local Answer known[8] = {};
     static thread_local int at = 0;
     const void *key = reinterpret_cast<const void *>(kernel);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-        cudaGetLastError();                              // not the next call's
-        return 0;
-    }
+    if (!allow_smem(kernel, kMostSmem)) return 0;
     int per_sm = 0;
     for (const Answer &k : known)
         if (k.kernel == key && k.threads == threads && k.smem == smem) per_sm = k.per_sm;

@@ -1,0 +1,90 @@
+"""Host threads that call the same operators at different sizes, each on its own stream.  The threads call the
+library itself, in a tight loop: the binding's Python part would run them mostly one after another."""
+import ctypes
+import threading
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+CALLS = 3000                                         # per thread
+
+
+class Call:
+    """One prepared call of the library: its arguments but the stream, the tensors they point into, its outputs."""
+
+    def __init__(self, fn, args, keep, outs):
+        self.fn, self.args, self.keep, self.outs = fn, args, keep, outs
+
+    def __call__(self, stream):
+        return self.fn(*self.args, stream)
+
+
+def _p(t):
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _run_together(calls):
+    """Every call CALLS times in a thread and on a stream of its own: none refused, and the last results those of
+    a call made alone."""
+    import torch
+    want = []
+    for c in calls:
+        assert c(None) == 0
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in c.outs])
+        for t in c.outs:
+            t.zero_()
+    torch.cuda.synchronize()
+    refused = [0] * len(calls)
+    streams = [torch.cuda.Stream() for _ in calls]
+    gate = threading.Barrier(len(calls))
+
+    def work(i):
+        call, stream = calls[i], ctypes.c_void_p(streams[i].cuda_stream)
+        gate.wait()
+        for _ in range(CALLS):
+            if call(stream) != 0:
+                refused[i] += 1
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not any(refused), f"calls refused per thread: {refused} of {CALLS}"
+    for c, w in zip(calls, want):
+        for a, b in zip(c.outs, w):
+            assert torch.equal(a, b)
+
+
+def _norm(op, d):
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    L, N = dbc.lib(), 3
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x, r = (torch.randn(N, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w = torch.randn(d, generator=g, device="cuda").bfloat16()
+    s, y = torch.empty_like(x), torch.empty_like(x)
+    q, sc, dw = torch.empty(N, d, dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda"), torch.empty(d, device="cuda")
+    ws = torch.empty(dbc.rms_norm_backward_workspace(N, d), dtype=torch.uint8, device="cuda")
+    eps = ctypes.c_float(1e-6)
+    keep = [x, r, w, ws]
+    if op == "norm":
+        return Call(L.rms_norm, (_p(x), d, 1, _p(r), d, _p(w), 1, N, d, eps, _p(s), d, _p(y), d, 1, None), keep, [s, y])
+    if op == "norm_i8":
+        return Call(L.rms_norm_i8, (_p(x), d, 1, _p(r), d, _p(w), 1, N, d, eps, _p(s), d, _p(q), d, _p(sc), None), keep,
+                    [s, q, sc])
+    if op == "quantize":
+        return Call(L.quantize_rows_i8, (_p(x), d, 1, N, d, _p(q), d, _p(sc), None), keep, [q, sc])
+    return Call(L.rms_norm_backward, (_p(x), d, 1, _p(r), d, 1, _p(w), 1, None, 0, N, d, eps, _p(y), d, _p(dw), _p(ws),
+                                      ws.numel(), None), keep, [y, dw])
+
+
+# pairs of widths that one kernel serves with different amounts of shared memory: wide rows, odd narrow rows
+# (tiles), odd wide rows
+@pytest.mark.parametrize("op", ["norm", "norm_i8", "quantize", "backward"])
+@pytest.mark.parametrize("widths", [(4096, 1536), (499, 301), (2047, 1027)])
+def test_norms_at_two_widths(op, widths):
+    _run_together([_norm(op, d) for d in widths] + [_norm(op, d) for d in widths])
