@@ -614,13 +614,15 @@ dbc_status run(const IN *H, const int64_t *offsets, int64_t rows, int64_t T, int
     const int chol_grid = (int)std::min<int64_t>(ns, (int64_t)sms * 4);
     const size_t smem_f = (size_t)(d + kSegMax) * (PW + 1) * sizeof(float);
     const size_t smem_i = (size_t)kSegMax * (PW + 1) * sizeof(float);
-    cudaFuncSetAttribute(chol_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_f);
-    cudaFuncSetAttribute(chol_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_i);
+    constexpr size_t kMostD = 512;                       // widest d of this path
+    if (!allow_smem(chol_kernel<false>, (kMostD + kSegMax) * (PW + 1) * sizeof(float)) ||
+        !allow_smem(chol_kernel<true>, smem_i) ||
+        !allow_smem(first_seg_kernel<IN>, 64 * 65 * sizeof(double) + 64 * (kMostD + 1) * sizeof(float)))
+        return DBC_ERR_CUDA;
     chol_kernel<false><<<chol_grid, 256, smem_f, stream>>>(L.segs, L.aug, L.gp, d, dR);
     ygram_kernel<<<dim3((unsigned)ns, 36), 256, 0, stream>>>(L.segs, L.aug, d, (float)c, L.gp);
     chol_kernel<true><<<chol_grid, 256, smem_i, stream>>>(L.segs, L.aug, L.gp, d, dR);
     const size_t smem1 = 64 * 65 * sizeof(double) + (size_t)64 * (d + 1) * sizeof(float);
-    cudaFuncSetAttribute(first_seg_kernel<IN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem1);
     first_seg_kernel<IN><<<(unsigned)std::min<int64_t>(ns, (int64_t)sms * 2), 256, smem1, stream>>>(
         H, d, L.segs, c, dR);
     count_launches(8);

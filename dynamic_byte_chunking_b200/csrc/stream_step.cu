@@ -217,11 +217,11 @@ extern "C" dbc_status chunk_coding_rate_step(const void *H, int dtype, int64_t s
     const size_t smem = ss::smem_bytes((int)d);
     const float sqrt_c = sqrtf((float)d / eps2);
     if (dtype == DBC_BF16) {
-        cudaFuncSetAttribute(ss::step_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (!allow_smem(ss::step_kernel<__nv_bfloat16>, ss::smem_bytes(ss::kMaxD))) return DBC_ERR_CUDA;
         ss::step_kernel<__nv_bfloat16><<<(unsigned)streams, ss::kThreads, smem, s>>>(
             static_cast<const __nv_bfloat16 *>(H), n, (int)d, sqrt_c, B_state, dR, dev_status);
     } else {
-        cudaFuncSetAttribute(ss::step_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (!allow_smem(ss::step_kernel<float>, ss::smem_bytes(ss::kMaxD))) return DBC_ERR_CUDA;
         ss::step_kernel<float><<<(unsigned)streams, ss::kThreads, smem, s>>>(static_cast<const float *>(H), n,
                                                                              (int)d, sqrt_c, B_state, dR,
                                                                              dev_status);

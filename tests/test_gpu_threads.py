@@ -88,3 +88,28 @@ def _norm(op, d):
 @pytest.mark.parametrize("widths", [(4096, 1536), (499, 301), (2047, 1027)])
 def test_norms_at_two_widths(op, widths):
     _run_together([_norm(op, d) for d in widths] + [_norm(op, d) for d in widths])
+
+
+def _coding_rate(d):
+    """The fp32 path (its factorisations' panels grow with d)."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(d)
+    H = torch.randn(70, d, generator=g, device="cuda").div(d ** 0.5)
+    dR = torch.empty(70, device="cuda")
+    ws = torch.empty(dbc.chunk_coding_rate_workspace(1, 70, 70, d), dtype=torch.uint8, device="cuda")
+    return Call(dbc.lib().chunk_coding_rate, (_p(H), 0, None, 1, 70, 70, d, ctypes.c_float(0.5), _p(dR), _p(ws), ws.numel(),
+                                              None), [H, ws], [dR])
+
+
+def _step(d):
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    H = torch.zeros(1, 1, d, device="cuda")          # zeros leave the carried factor as it is
+    B, dR = torch.eye(d, device="cuda"), torch.empty(1, device="cuda")
+    return Call(dbc.lib().chunk_coding_rate_step, (_p(H), 0, 1, 1, d, ctypes.c_float(0.5), _p(B), _p(dR), None), [H, B], [dR])
+
+
+@pytest.mark.parametrize("make,sizes", [(_coding_rate, (512, 64)), (_step, (256, 64))], ids=["coding_rate", "step"])
+def test_chunker_at_two_sizes(make, sizes):
+    _run_together([make(n) for n in sizes] + [make(n) for n in sizes])
