@@ -15,16 +15,32 @@ using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, vo
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+inline void *driver_entry(const char *name) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess
+               ? p : nullptr;
+}
+
+// The encoder, or NULL.  It is a driver call and needs a context on the calling host thread, which a
+// thread whose first CUDA call this is does not have yet: the runtime's device is then made current (legal
+// in a stream capture; a context that is there already stays).
 inline EncodeFn encoder() {
+    using CurrentFn = CUresult (*)(CUcontext *);
     static EncodeFn fn = nullptr;
+    static CurrentFn current = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeFn>(p);
+        fn = reinterpret_cast<EncodeFn>(driver_entry("cuTensorMapEncodeTiled"));
+        current = reinterpret_cast<CurrentFn>(driver_entry("cuCtxGetCurrent"));
     });
+    CUcontext ctx = nullptr;
+    int dev = 0;
+    if (current && (current(&ctx) != CUDA_SUCCESS || !ctx) &&
+        (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)) {
+        cudaGetLastError();                              // not the next call's
+        return nullptr;
+    }
     return fn;
 }
 

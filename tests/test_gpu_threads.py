@@ -113,3 +113,70 @@ def _step(d):
 @pytest.mark.parametrize("make,sizes", [(_coding_rate, (512, 64)), (_step, (256, 64))], ids=["coding_rate", "step"])
 def test_chunker_at_two_sizes(make, sizes):
     _run_together([make(n) for n in sizes] + [make(n) for n in sizes])
+
+
+def _product(M, N, K):
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a, b = (torch.randint(-127, 128, (R, K), generator=g, device="cuda", dtype=torch.int8) for R in (M, N))
+    sa, sb = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    out = torch.empty(M, N, device="cuda")
+    return Call(dbc.lib().matmul_i8, (_p(a), K, _p(sa), _p(b), K, _p(sb), None, 0, M, N, K, _p(out), N, 0, None),
+                [a, b, sa, sb], [out])
+
+
+def _upsample():
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    T, K, d = 128, 32, 256
+    H, G = (torch.randn(n, d, generator=g, device="cuda").bfloat16() for n in (T, K))
+    W = torch.randn(16, d, d, generator=g, device="cuda").bfloat16()
+    idx, io = torch.arange(0, T, T // K, device="cuda"), torch.tensor([0, K], device="cuda")
+    S = torch.empty(T, d, device="cuda")
+    ws = torch.empty(dbc.chunk_upsample_workspace(1, T, 16), dtype=torch.uint8, device="cuda")
+    return Call(dbc.lib().chunk_upsample, (_p(G), d, _p(H), 1, None, T, T, d, _p(idx), _p(io), 1, _p(W), 16, 0, _p(S), _p(ws),
+                                           ws.numel(), None), [H, G, W, idx, io, ws], [S])
+
+
+def _tensor_rate():
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(2)
+    T, d = 512, 256
+    H = torch.randn(T, d, generator=g, device="cuda").div(16).bfloat16()
+    dR = torch.empty(T, device="cuda")
+    ws = torch.empty(dbc.chunk_coding_rate_workspace(1, T, T, d), dtype=torch.uint8, device="cuda")
+    return Call(dbc.lib().chunk_coding_rate, (_p(H), 1, None, 1, T, T, d, ctypes.c_float(0.5), _p(dR), _p(ws), ws.numel(), None),
+                [H, ws], [dR])
+
+
+@pytest.mark.parametrize("make", [lambda: _product(5, 256, 512), lambda: _product(1500, 1536, 256), _upsample, _tensor_rate],
+                         ids=["product_split", "product_wide", "upsample", "coding_rate"])
+def test_first_cuda_call_of_a_thread(make):
+    """A host thread that has made no CUDA call yet: the same kernels and results as in any other."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    call = make()
+    before = dbc.launch_count()
+    assert call(None) == 0
+    launches = dbc.launch_count() - before
+    torch.cuda.synchronize()
+    want = [t.clone() for t in call.outs]
+    for t in call.outs:
+        t.zero_()
+    torch.cuda.synchronize()
+    rc = []
+    before = dbc.launch_count()
+    t = threading.Thread(target=lambda: rc.append(call(None)))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert rc == [0] and dbc.launch_count() - before == launches
+    for a, b in zip(call.outs, want):
+        assert torch.equal(a, b)
+
+
+def test_products_at_several_sizes():
+    _run_together([_product(5, 256, 512), _product(14, 1536, 256), _product(130, 300, 256), _product(1500, 1536, 256)])
