@@ -343,6 +343,14 @@ __device__ __forceinline__ void bwd_stats_wide(const Frag<TY, NE> &y, const Frag
         sg += (double)g * v;
     }
 }
+// Whether the fragment has a g = dy w that is not zero.
+template <class TY, int NE>
+__device__ __forceinline__ bool any_g(const Frag<TY, NE> &y, const float (&w)[NE]) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) any |= y.at(i) * w[i] != 0.f;
+    return any;
+}
 template <class Q, bool DW, class TY, class T, int NE>
 __device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int stage, T *dx, int j, int threads,
                                          const Frag<TY, NE> &y, const Frag<T, NE> &f, const float (&w)[NE],
@@ -412,13 +420,20 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
         for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], pss, psg);
         const float ss = team_reduce<W>(pss.x + pss.y, Add()), sg = team_reduce<W>(psg.x + psg.y, Add());
         BwdFactor k(ss, sg, a);
-        if (__any_sync(0xffffffffu, !in_range(ss, sg))) {
+        bool odd = !in_range(ss, sg);
+        if (__any_sync(0xffffffffu, faint(sg))) {
+            bool some = false;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) some |= any_g(y[j], w[j]);
+            odd |= team_any<W>(some) && faint(sg);
+        }
+        if (__any_sync(0xffffffffu, odd)) {
             double s2 = 0, g2 = 0;
 #pragma unroll
             for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
             s2 = team_reduce<W>(s2, Add());
             g2 = team_reduce<W>(g2, Add());
-            if (!in_range(ss, sg)) k = BwdFactor(s2, g2, a);   // not the warp's other rows
+            if (odd) k = BwdFactor(s2, g2, a);           // not the warp's other rows
             if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
         }
 #pragma unroll
@@ -494,7 +509,14 @@ __global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
         ss = team_reduce<32>(v.x, Add());
         sg = team_reduce<32>(v.y, Add());
         BwdFactor k(ss, sg, a);
-        if (!in_range(ss, sg)) {     // the same in every thread
+        bool odd = !in_range(ss, sg);                    // the same in every thread
+        if (faint(sg)) {
+            bool some = false;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) some |= any_g(y[j], w[j]);
+            odd |= __syncthreads_or(some) != 0;
+        }
+        if (odd) {
             double s2 = 0, g2 = 0;
 #pragma unroll
             for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);

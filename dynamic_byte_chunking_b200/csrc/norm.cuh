@@ -297,6 +297,13 @@ __device__ __forceinline__ V team_reduce(V v, F f) {
     return v;
 }
 
+// Whether `v` holds in any lane of the team (all 32 lanes take part).
+template <int W>
+__device__ __forceinline__ bool team_any(bool v) {
+    const uint32_t b = __ballot_sync(0xffffffffu, v);
+    return ((b >> (threadIdx.x & 31 & ~(W - 1))) & (0xffffffffu >> (32 - W))) != 0;
+}
+
 // ---------------------------------------------------------------- what the kernels share
 template <class T>
 __device__ __forceinline__ float round_to(float v);
@@ -366,6 +373,10 @@ struct BwdArgs {
 };
 
 __device__ __forceinline__ bool in_range(float ss, float sg) { return ss >= kLow && ss <= kHigh && isfinite(sg); }
+// sum(g s) that is this small may have lost products below fp32's range: each loses up to 2^-150, up to 2^-136
+// over the longest row, which a sum of 2^-110 does not notice (2^-26 of it).  Such a row is summed again in fp64
+// unless all its g are zero (padding), where the fp32 sum is exact.
+__device__ __forceinline__ bool faint(float sg) { return fabsf(sg) < 0x1p-110f; }
 
 // dx = rstd (g - xhat c) + ds with xhat = s rstd and c = mean(g xhat); rstd as in RowFactor.
 struct BwdFactor {

@@ -418,7 +418,14 @@ __global__ void __launch_bounds__(kThreads) odd_bwd_tile_kernel(const BwdArgs a,
             ss = team_reduce<W>(ss, Add());
             sg = team_reduce<W>(sg, Add());
             BwdFactor b(ss, sg, a);
-            const bool odd = k < rows && !in_range(ss, sg);
+            bool odd = !in_range(ss, sg);
+            if (__any_sync(0xffffffffu, faint(sg))) {
+                bool some = false;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) some |= y[j] * w[j] != 0.f;
+                odd |= team_any<W>(some) && faint(sg);
+            }
+            odd &= k < rows;
             if (__any_sync(0xffffffffu, odd)) {
                 double s2 = 0, g2 = 0;
 #pragma unroll
@@ -523,7 +530,14 @@ __global__ void __launch_bounds__(MAXT) odd_bwd_kernel(const BwdArgs a, int yslo
         }
         p = team_pair(p, Add(), Add(), sh);       // (its barrier: everybody has read s)
         BwdFactor k(p.x, p.y, a);
-        if (!in_range(p.x, p.y)) {                       // the same in the whole team
+        bool odd = !in_range(p.x, p.y);                  // the same in the whole team
+        if (faint(p.y)) {
+            bool some = false;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) some |= y[j] * w[j] != 0.f;
+            odd |= __syncthreads_or(some) != 0;
+        }
+        if (odd) {
             double2 q = make_double2(0, 0);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {

@@ -458,7 +458,8 @@ DBC_API dbc_status quantize_rows_i8(const void *x, int64_t x_stride, int dtype, 
  * With g = dy * w and xhat = s * rstd (rstd recomputed from s):
  *   dx = rstd * (g - xhat * mean(g * xhat)) + ds,   dw = sum over rows of dy * xhat.
  * dx is the gradient of x and, equally, of the residual; ds is the gradient
- * that reaches the stored sum from elsewhere (the residual stream).
+ * that reaches the stored sum from elsewhere (the residual stream).  Row sums
+ * whose terms leave fp32's range are taken in fp64; dy * w is rounded to fp32.
  *
  * dy       [N, d] fp32 or bf16 (dy_dtype), dy_stride.
  * s        [N, d] (dtype): rms_norm's s, or its x when there was no residual.

@@ -506,3 +506,31 @@ def test_sum_that_is_not_stored(d):
                          sc2.data_ptr(), None, st) == 0
     # (q2's rows are d bytes apart, q's on 16-byte boundaries: two routes through memory, the same codes)
     assert torch.equal(y, y2) and torch.equal(q, q2) and torch.allclose(sc, sc2, rtol=1e-6)
+
+
+@pytest.mark.parametrize("T", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [40, 200, 256, 512, 1000, 2048, 8192, 33, 257, 500, 777, 1531, 3001])
+def test_gradients_whose_products_leave_fp32(T, d):
+    """dy so small that dy w s vanishes in fp32 while dy and s do not: the projection term of dx stays.  Rows of
+    zeros, rows with one such gradient and ordinary rows between them (bounds: backward_bounds)."""
+    import dynamic_byte_chunking_b200 as dbc
+    rng = np.random.default_rng(d)
+    N = 11
+    s, dy = _vals(rng, (N, d), T), _vals(rng, (N, d), T)
+    for r, es, ey in ((0, -50, -106), (2, -45, -100), (3, -40, -118), (4, -50, -60), (7, -49, -110), (10, -48, -104)):
+        s[r], dy[r] = o.store(s[r] * 2.0 ** es, T), o.store(dy[r] * 2.0 ** ey, T)
+    dy[5] = 0
+    dy[7, 1:] = 0
+    w = _weight(rng, d, T)
+    st = _status()
+    for eps in (1e-30, EPS):
+        dx, dw = dbc.rms_norm_backward(_t(dy, T), _t(s, T), _t(w, T), eps=eps, dev_status=st)
+        rx, rw = o.rms_norm_backward(dy, s, w, eps, None)
+        bx, bw = o.backward_bounds(dy, s, w, eps, None, T)
+        # Below 2^-126 fp32 has a step of 2^-149: dy w, its difference from xhat c and c itself are each off by half
+        # of it there, whatever their size (an element of row 3 that is 2^-8 of the others is there), and dx is
+        # rstd times that.
+        rs = o.rstd_of(s, eps)
+        _close(dx, rx, bx + rs * 2.0 ** -150 * (2 + np.abs(s * rs)), f"dx eps={eps}")
+        _close(dw, rw, bw, f"dw eps={eps}")
+    assert st.item() == 0
