@@ -61,10 +61,14 @@ __device__ __forceinline__ void stats(const Frag<T, NE> &f, const float (&w)[NE]
     }
 }
 
+// More dynamic shared memory than any launch here asks for (the tiles of odd rows take up to 197 KB, at eight
+// rows of 1024 fp32 elements), and with what the kernels declare beside it within a CTA's 227 KB.
+constexpr int kMostSmem = 208 * 1024;
+
 // Rows in shared memory at a time of kernels that copy ahead: B bytes per thread and row, up to MAXT
-// threads; 64 KB a CTA of 256 threads (three to an SM), and what fits for the wide ones.
-constexpr int block_stages(int B, int MAXT) {
-    const int s = MAXT > 256 ? 200 * 1024 / (B * MAXT) : 64 * 1024 / (B * MAXT);
+// threads; 64 KB a CTA of 256 threads (three to an SM), and what fits beside `other` bytes for the wide ones.
+constexpr int block_stages(int B, int MAXT, int other = 0) {
+    const int s = MAXT > 256 ? (kMostSmem - other) / (B * MAXT) : 64 * 1024 / (B * MAXT);
     return s < 1 ? 1 : s > 4 ? 4 : s;
 }
 
@@ -272,12 +276,17 @@ __global__ void __launch_bounds__(MAXT) block_kernel(const FwdArgs a) {
     }
 }
 
-// The same for the backward pass: dy, s and ds of a thread's row.
-template <class TY, class T, int NE, int NV, int MAXT>
+// The same for the backward pass: dy, s and ds of a thread's row; SUMS: with the fp64 sums of the threads' columns
+// behind them.
+template <class TY, class T, int NE, int NV, int MAXT, bool SUMS>
 struct Ring {
     static constexpr int UY = NE * (int)sizeof(TY), U = NE * (int)sizeof(T), kS = NV * UY, kDs = kS + NV * U;
-    static constexpr int B = kDs + NV * U, S = block_stages(B, MAXT);
-    static constexpr int smem(int threads) { return S * B * threads; }
+    static constexpr int kSums = SUMS ? NV * NE * (int)sizeof(double) : 0;          // of a thread
+    static constexpr int B = kDs + NV * U, S = block_stages(B, MAXT, kSums * MAXT);
+    static constexpr int smem(int threads) { return (S * B + kSums) * threads; }
+    static __device__ __forceinline__ double *sums(char *smem, int threads) {
+        return reinterpret_cast<double *>(smem + S * B * threads);
+    }
     // Where the next row to copy lies; advanced by `step` rows at a time (pointers, not products of rows
     // and strides: three of those a row were a tenth of the instructions).
     struct Walk {
@@ -384,14 +393,16 @@ __device__ __forceinline__ void bwd_frag(const BwdArgs &a, const char *smem, int
 }
 
 // Teams of W lanes walk the rows; a lane keeps the dw sums of its own columns
-// in registers, the CTA joins them at the end (a fixed order).
+// (fp32 in registers, fp64 in shared memory behind the ring), the CTA joins
+// them at the end (a fixed order).
 template <class TY, class T, int NE, bool DW, int W, int NV>
-__global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
-    using Q = Ring<TY, T, NE, NV, kThreads>;
+__global__ void __launch_bounds__(kThreads, 2) bwd_team_kernel(const BwdArgs a) {
+    using Q = Ring<TY, T, NE, NV, kThreads, DW>;
     extern __shared__ __align__(16) char smem[];
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-    const int t = threadIdx.x % W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = threadIdx.x % W, lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * (kThreads / W);
+    double *const sums = Q::sums(smem, kThreads);         // element i of fragment j at (j * NE + i) * kThreads + thread
     float w[NV][NE], acc[NV][NE];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -406,74 +417,80 @@ __global__ void __launch_bounds__(kThreads) bwd_team_kernel(const BwdArgs a) {
     T *px = static_cast<T *>(a.dx) + (first + mine) * a.xs;
     const int64_t dpx = step * a.xs;
     for (int k = 0; k < Q::S - 1; ++k) Q::start(a, walk, base, k, t, W, kThreads);
+    if (DW) {
+#pragma unroll
+        for (int i = 0; i < NV * NE; ++i) sums[i * kThreads + threadIdx.x] = 0;
+    }
     int stage = 0;
-    for (int64_t rw = first; rw < a.N; rw += step, px += dpx) {
-        const int64_t r = rw + mine;
-        Q::start(a, walk, base, stage == 0 ? Q::S - 1 : stage - 1, t, W, kThreads);
-        Q::wait();
-        Frag<TY, NE> y[NV];
-        Frag<T, NE> f[NV];
-        float2 pss = make_float2(0.f, 0.f), psg = pss;
+    for (int64_t rw = first; rw < a.N;) {
+        // kFold rows at a time (all of them where no dw is wanted), then the fold
+        const int64_t end = DW ? min(a.N, rw + kFold * step) : a.N;
+        for (; rw < end; rw += step, px += dpx) {
+            const int64_t r = rw + mine;
+            Q::start(a, walk, base, stage == 0 ? Q::S - 1 : stage - 1, t, W, kThreads);
+            Q::wait();
+            Frag<TY, NE> y[NV];
+            Frag<T, NE> f[NV];
+            float2 pss = make_float2(0.f, 0.f), psg = pss;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) Q::get(smem, stage, j, kThreads, y[j], f[j]);
+            for (int j = 0; j < NV; ++j) Q::get(smem, stage, j, kThreads, y[j], f[j]);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], pss, psg);
-        const float ss = team_reduce<W>(pss.x + pss.y, Add()), sg = team_reduce<W>(psg.x + psg.y, Add());
-        BwdFactor k(ss, sg, a);
-        bool odd = !in_range(ss, sg);
-        if (__any_sync(0xffffffffu, faint(sg))) {
-            bool some = false;
+            for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], pss, psg);
+            const float ss = team_reduce<W>(pss.x + pss.y, Add()), sg = team_reduce<W>(psg.x + psg.y, Add());
+            BwdFactor k(ss, sg, a);
+            bool odd = !in_range(ss, sg);
+            if (__any_sync(0xffffffffu, faint(sg))) {
+                bool some = false;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) some |= any_g(y[j], w[j]);
-            odd |= team_any<W>(some) && faint(sg);
+                for (int j = 0; j < NV; ++j) some |= any_g(y[j], w[j]);
+                odd |= team_any<W>(some) && faint(sg);
+            }
+            if (__any_sync(0xffffffffu, odd)) {
+                double s2 = 0, g2 = 0;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
+                s2 = team_reduce<W>(s2, Add());
+                g2 = team_reduce<W>(g2, Add());
+                if (odd) k = BwdFactor(s2, g2, a);           // not the warp's other rows
+                if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (j * W + t) * NE;
+                // read again rather than held (100000 x 512 with ds: 67 us against 71, which spilled)
+                if constexpr (NV > 1) Q::get(smem, stage, j, kThreads, y[j], f[j]);
+                if (r < a.N && col < a.d)
+                    bwd_frag<Q, DW>(a, smem, stage, px + col, j, kThreads, y[j], f[j], w[j], k, acc[j]);
+            }
+            if (++stage == Q::S) stage = 0;
         }
-        if (__any_sync(0xffffffffu, odd)) {
-            double s2 = 0, g2 = 0;
+        if (DW) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
-            s2 = team_reduce<W>(s2, Add());
-            g2 = team_reduce<W>(g2, Add());
-            if (odd) k = BwdFactor(s2, g2, a);           // not the warp's other rows
-            if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
+            for (int j = 0; j < NV; ++j)
+                fold_sums<NE, false>(sums + j * NE * kThreads + threadIdx.x, kThreads, acc[j], false);
         }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (j * W + t) * NE;
-            if (r < a.N && col < a.d)
-                bwd_frag<Q, DW>(a, smem, stage, px + col, j, kThreads, y[j], f[j], w[j], k, acc[j]);
-        }
-        if (++stage == Q::S) stage = 0;
     }
     if constexpr (DW) {
-        // the ring's room, a line per warp (a stage alone holds at least 4 bytes per column and warp)
-        constexpr int LINE = NV * W * NE;
-        static_assert(Q::smem(kThreads) >= kThreads / 32 * LINE * 4, "");
-        float *const sm = reinterpret_cast<float *>(smem);
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                float v = acc[j][i];
-#pragma unroll
-                for (int o = W; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane < W) sm[warp * LINE + (j * W + t) * NE + i] = v;
-            }
         __syncthreads();
         for (int c = threadIdx.x; c < a.d; c += kThreads) {
-            float v = 0.f;
+            const int v = c / NE, e = c % NE;            // lane v % W's fragment v / W has the column
+            const double *const at = sums + (v / W * NE + e) * kThreads + v % W;
+            double sum = 0;
 #pragma unroll
-            for (int k = 0; k < kThreads / 32; ++k) v += sm[k * LINE + c];
-            a.part[(int64_t)blockIdx.x * a.d + c] = v;
+            for (int k = 0; k < kThreads / W; ++k) sum += at[k * W];
+            a.part[(int64_t)blockIdx.x * a.d + c] = sum;
         }
     }
 }
 
-// Wide rows: one row per CTA at a time, NV fragments per thread.
+// Wide rows: one row per CTA at a time, NV fragments per thread.  A thread's fp64 dw sums are in shared memory
+// behind the ring or, where that has no room for them (1024 threads), its columns of the CTA's line.  In the
+// line element i of fragment v, of V of them, is at i * V + v: whole sectors to a warp.
 template <class TY, class T, int NE, bool DW, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
-    using Q = Ring<TY, T, NE, NV, MAXT>;
+__global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 0)     // (unbounded, 1024 threads got 32 registers and spilled)
+    bwd_block_kernel(const BwdArgs a) {
+    constexpr bool OWN = DW && MAXT <= 512;
+    using Q = Ring<TY, T, NE, NV, MAXT, OWN>;
     extern __shared__ __align__(16) char smem[];
     __shared__ float2 part[2][32];
     __shared__ double2 wide[32];
@@ -491,76 +508,91 @@ __global__ void __launch_bounds__(MAXT) bwd_block_kernel(const BwdArgs a) {
     T *px = static_cast<T *>(a.dx) + (int64_t)blockIdx.x * a.xs;
     const int64_t dpx = (int64_t)gridDim.x * a.xs;
     for (int k = 0; k < Q::S - 1; ++k) Q::start(a, walk, base, k, t, W, W);
+    double *const sums = Q::sums(smem, W), *const line = DW ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
+    const int V = a.d / NE;
     int ph = 0, stage = 0;
-    for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, ph ^= 1, px += dpx) {
-        Q::start(a, walk, base, stage == 0 ? Q::S - 1 : stage - 1, t, W, W);
-        Q::wait();
-        Frag<TY, NE> y[NV];
-        Frag<T, NE> f[NV];
-        float2 pss = make_float2(0.f, 0.f), psg = pss;
+    bool first = true;
+    for (int64_t r = blockIdx.x; r < a.N; first = false) {
+        // kFold rows at a time (all of them where no dw is wanted), then the fold
+        const int64_t end = DW ? min(a.N, r + kFold * (int64_t)gridDim.x) : a.N;
+        for (; r < end; r += gridDim.x, ph ^= 1, px += dpx) {
+            Q::start(a, walk, base, stage == 0 ? Q::S - 1 : stage - 1, t, W, W);
+            Q::wait();
+            Frag<TY, NE> y[NV];
+            Frag<T, NE> f[NV];
+            float2 pss = make_float2(0.f, 0.f), psg = pss;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) Q::get(smem, stage, j, W, y[j], f[j]);
+            for (int j = 0; j < NV; ++j) Q::get(smem, stage, j, W, y[j], f[j]);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], pss, psg);
-        float ss = team_reduce<32>(pss.x + pss.y, Add()), sg = team_reduce<32>(psg.x + psg.y, Add());
-        if (lane == 0) part[ph][warp] = make_float2(ss, sg);
-        __syncthreads();             // the other buffer's readers are past the row before's barrier
-        const float2 v = lane < warps ? part[ph][lane] : make_float2(0.f, 0.f);
-        ss = team_reduce<32>(v.x, Add());
-        sg = team_reduce<32>(v.y, Add());
-        BwdFactor k(ss, sg, a);
-        bool odd = !in_range(ss, sg);                    // the same in every thread
-        if (faint(sg)) {
-            bool some = false;
+            for (int j = 0; j < NV; ++j) bwd_stats(y[j], f[j], w[j], pss, psg);
+            float ss = team_reduce<32>(pss.x + pss.y, Add()), sg = team_reduce<32>(psg.x + psg.y, Add());
+            if (lane == 0) part[ph][warp] = make_float2(ss, sg);
+            __syncthreads();             // the other buffer's readers are past the row before's barrier
+            const float2 v = lane < warps ? part[ph][lane] : make_float2(0.f, 0.f);
+            ss = team_reduce<32>(v.x, Add());
+            sg = team_reduce<32>(v.y, Add());
+            BwdFactor k(ss, sg, a);
+            bool odd = !in_range(ss, sg);                    // the same in every thread
+            if (faint(sg)) {
+                bool some = false;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) some |= any_g(y[j], w[j]);
-            odd |= __syncthreads_or(some) != 0;
+                for (int j = 0; j < NV; ++j) some |= any_g(y[j], w[j]);
+                odd |= __syncthreads_or(some) != 0;
+            }
+            if (odd) {
+                double s2 = 0, g2 = 0;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
+                s2 = team_reduce<32>(s2, Add());
+                g2 = team_reduce<32>(g2, Add());
+                if (lane == 0) wide[warp] = make_double2(s2, g2);
+                __syncthreads();
+                const double2 v2 = lane < warps ? wide[lane] : make_double2(0, 0);
+                s2 = team_reduce<32>(v2.x, Add());
+                g2 = team_reduce<32>(v2.y, Add());
+                k = BwdFactor(s2, g2, a);
+                if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (j * W + t) * NE;
+                if (col < a.d) {
+                    // Fragments are read again after the barrier rather than held across it (20000 x 4096 bf16: 109
+                    // us against 114; 8192 x 16384 with fp32 dy: 419 against 505), but for fp32 dy at up to 256 threads,
+                    // where that costs (32749 x 1536: 95 against 87)
+                    if constexpr (sizeof(TY) == 2 || MAXT > 256) Q::get(smem, stage, j, W, y[j], f[j]);
+                    bwd_frag<Q, DW>(a, smem, stage, px + col, j, W, y[j], f[j], w[j], k, acc[j]);
+                }
+            }
+            if (++stage == Q::S) stage = 0;
         }
-        if (odd) {
-            double s2 = 0, g2 = 0;
+        if (DW) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) bwd_stats_wide(y[j], f[j], w[j], s2, g2);
-            s2 = team_reduce<32>(s2, Add());
-            g2 = team_reduce<32>(g2, Add());
-            if (lane == 0) wide[warp] = make_double2(s2, g2);
-            __syncthreads();
-            const double2 v2 = lane < warps ? wide[lane] : make_double2(0, 0);
-            s2 = team_reduce<32>(v2.x, Add());
-            g2 = team_reduce<32>(v2.y, Add());
-            k = BwdFactor(s2, g2, a);
-            if (t == 0 && (!isfinite(s2) || !isfinite(g2))) flag(a.st, DBC_ERR_NONFINITE);
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (j * W + t) * NE;
-            if (col < a.d) {
-                // bf16 fragments are read again after the barrier rather than held across it (20000 x 4096:
-                // 109 us against 114); with fp32 dy that costs (32749 x 1536: 95 against 87)
-                if constexpr (sizeof(TY) == 2) Q::get(smem, stage, j, W, y[j], f[j]);
-                bwd_frag<Q, DW>(a, smem, stage, px + col, j, W, y[j], f[j], w[j], k, acc[j]);
+            for (int j = 0; j < NV; ++j) {
+                if (OWN) fold_sums<NE, false>(sums + j * NE * W + t, W, acc[j], first);
+                else if (j * W + t < V) fold_sums<NE, true>(line + j * W + t, V, acc[j], first);
             }
         }
-        if (++stage == Q::S) stage = 0;
     }
-    if constexpr (DW) {
+    if (OWN) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
+            if (j * W + t < V) {
 #pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                const int col = (j * W + t) * NE + i;
-                if (col < a.d) a.part[(int64_t)blockIdx.x * a.d + col] = acc[j][i];
+                for (int i = 0; i < NE; ++i) line[i * V + j * W + t] = sums[(j * NE + i) * W + t];
             }
     }
 }
 
-// dw = the CTAs' lines added up, in a fixed order: 8 columns (one 32-byte
-// sector of every line) per CTA, 128 threads per column.
-__global__ void __launch_bounds__(1024) dw_kernel(const float *part, int lines, int d, float *dw) {
+// dw = the CTAs' lines added up, in a fixed order: 8 columns (two 32-byte
+// sectors of every line) per CTA, 128 threads per column.  The lines hold
+// element i of fragment v, of V of them, at i * V + v.
+__global__ void __launch_bounds__(1024) dw_kernel(const double *part, int lines, int d, int V, float *dw) {
     __shared__ double sm[32][8];
     const int c = threadIdx.x & 7, k = threadIdx.x >> 3, col = blockIdx.x * 8 + c;
-    float v[10];                                     // lines <= 148 * 8 < 128 * 10
+    double v[10];                                    // lines <= 148 * 8 < 128 * 10
 #pragma unroll
-    for (int i = 0; i < 10; ++i) v[i] = col < d && k + i * 128 < lines ? part[(int64_t)(k + i * 128) * d + col] : 0.f;
+    for (int i = 0; i < 10; ++i) v[i] = col < d && k + i * 128 < lines ? part[(int64_t)(k + i * 128) * d + col] : 0.0;
     double t = 0;
 #pragma unroll
     for (int i = 0; i < 10; ++i) t += v[i];
@@ -571,7 +603,7 @@ __global__ void __launch_bounds__(1024) dw_kernel(const float *part, int lines, 
     if (threadIdx.x < 256) {                         // warp w: column w
         t = team_reduce<32>(sm[threadIdx.x & 31][threadIdx.x >> 5], Add());
         const int out = blockIdx.x * 8 + (threadIdx.x >> 5);
-        if ((threadIdx.x & 31) == 0 && out < d) dw[out] = (float)t;
+        if ((threadIdx.x & 31) == 0 && out < d) dw[out % V * (d / V) + out / V] = (float)t;
     }
 }
 
@@ -619,10 +651,6 @@ dbc_status launch_team(const FwdArgs &a, cudaStream_t st) {
 // each host thread remembers its last answers (they depend on the kernel and
 // the launch alone).
 constexpr int kSms = 148;
-// More dynamic shared memory than any launch here asks for (block_stages allows 200 KB; the tiles of odd rows
-// take up to 197 KB, at eight rows of 1024 fp32 elements), and with the 16 KB of static shared memory that one
-// kernel has beside it within a CTA's 227 KB.
-constexpr int kMostSmem = 208 * 1024;
 template <class K>
 int resident(K kernel, int threads, int smem, int64_t most) {
     struct Answer {
@@ -777,7 +805,8 @@ int launch_resident(K kernel, const BwdArgs &a, int threads, int smem, int64_t m
 template <class TY, class T, int NV, int MAXT>
 int launch_odd_bwd_row(const BwdArgs &a, cudaStream_t st) {
     const int yslot = slot_bytes(a.d, sizeof(TY)), slot = slot_bytes(a.d, sizeof(T));
-    const OddPlan p = odd_plan(a.d, NV, yslot + (a.ds ? 2 : 1) * slot, 0);
+    const int sums = a.part && NV <= 8 ? (a.d + NV * 32 - 1) / (NV * 32) * 32 * NV * (int)sizeof(double) : 0;
+    const OddPlan p = odd_plan(a.d, NV, yslot + (a.ds ? 2 : 1) * slot, sums);
     auto *k = a.part ? odd_bwd_kernel<TY, T, true, NV, MAXT> : odd_bwd_kernel<TY, T, false, NV, MAXT>;
     const int ctas = resident(k, p.threads, p.smem, bwd_lines(a.N, a.d));
     if (ctas) k<<<ctas, p.threads, p.smem, st>>>(a, yslot, slot, p.stages);
@@ -787,7 +816,9 @@ template <class TY, class T, int W, int NV>
 int launch_odd_bwd_tile(const BwdArgs &a, cudaStream_t st) {
     const int yslot = slot_bytes(a.d, sizeof(TY)), slot = slot_bytes(a.d, sizeof(T));
     const int row = 2 * (yslot + (a.ds ? 2 : 1) * slot) + slot;
-    const int R = odd_tile_rows(a.N, row, kThreads / W, 92 * 1024), smem = R * row;
+    const int sums = a.part ? (a.d + W - 1) / W * kThreads * (int)sizeof(double) : 0;
+    const int R = std::min(kFold * kThreads / W, odd_tile_rows(a.N, row, kThreads / W, 112 * 1024 - sums));
+    const int smem = sums + R * row;
     auto *k = a.part ? odd_bwd_tile_kernel<TY, T, true, W, NV> : odd_bwd_tile_kernel<TY, T, false, W, NV>;
     const int ctas = resident(k, kThreads, smem, std::min<int64_t>(bwd_lines(a.N, a.d), (a.N + R - 1) / R));
     if (ctas) k<<<ctas, kThreads, smem, st>>>(a, R, yslot, slot);
@@ -796,28 +827,33 @@ int launch_odd_bwd_tile(const BwdArgs &a, cudaStream_t st) {
 
 template <class TY, class T, int NE, int W, int NV>
 int launch_bwd_team(const BwdArgs &a, cudaStream_t st) {
-    const int smem = Ring<TY, T, NE, NV, kThreads>::smem(kThreads);
     constexpr int rows = kThreads / W;
     const int64_t most = std::min<int64_t>(bwd_lines(a.N, a.d), (a.N + rows - 1) / rows);
-    return a.part ? launch_resident(bwd_team_kernel<TY, T, NE, true, W, NV>, a, kThreads, smem, most, st)
-                  : launch_resident(bwd_team_kernel<TY, T, NE, false, W, NV>, a, kThreads, smem, most, st);
+    return a.part ? launch_resident(bwd_team_kernel<TY, T, NE, true, W, NV>, a, kThreads,
+                                    Ring<TY, T, NE, NV, kThreads, true>::smem(kThreads), most, st)
+                  : launch_resident(bwd_team_kernel<TY, T, NE, false, W, NV>, a, kThreads,
+                                    Ring<TY, T, NE, NV, kThreads, false>::smem(kThreads), most, st);
 }
 
 template <class TY, class T, int NE, int NV, int MAXT>
 int launch_bwd_block(const BwdArgs &a, cudaStream_t st) {
     const int threads = ((a.d + NE * NV - 1) / (NE * NV) + 31) / 32 * 32;
-    const int smem = Ring<TY, T, NE, NV, MAXT>::smem(threads), most = bwd_lines(a.N, a.d);
-    return a.part ? launch_resident(bwd_block_kernel<TY, T, NE, true, NV, MAXT>, a, threads, smem, most, st)
-                  : launch_resident(bwd_block_kernel<TY, T, NE, false, NV, MAXT>, a, threads, smem, most, st);
+    const int most = bwd_lines(a.N, a.d);
+    return a.part ? launch_resident(bwd_block_kernel<TY, T, NE, true, NV, MAXT>, a, threads,
+                                    Ring<TY, T, NE, NV, MAXT, MAXT <= 512>::smem(threads), most, st)
+                  : launch_resident(bwd_block_kernel<TY, T, NE, false, NV, MAXT>, a, threads,
+                                    Ring<TY, T, NE, NV, MAXT, false>::smem(threads), most, st);
 }
 
+// (V: fragments of a line, see dw_kernel)
 template <class TY, class T>
-int launch_bwd(const BwdArgs &a, cudaStream_t st) {
+int launch_bwd(const BwdArgs &a, int &V, cudaStream_t st) {
     constexpr int E = 16 / sizeof(T);
     const int64_t e = sizeof(T), ey = sizeof(TY);
     const bool vec = a.d % E == 0 && on_grid(a.s, a.ss, e, 16) && on_grid(a.ds, a.ds_s, e, 16) &&
                      on_grid(a.dx, a.xs, e, 16) && on_grid(a.dy, a.ys, ey, std::min<int64_t>(16, E * ey)) &&
                      on_grid(a.w.p, 0, 1, a.w.bf16 ? E * 2 : 16);
+    V = a.d;
     if (!vec) {
         if (a.d <= 64) return launch_odd_bwd_tile<TY, T, 8, 8>(a, st);
         if (a.d <= 128) return launch_odd_bwd_tile<TY, T, 16, 8>(a, st);
@@ -827,11 +863,11 @@ int launch_bwd(const BwdArgs &a, cudaStream_t st) {
         if (a.d <= 8192) return launch_odd_bwd_row<TY, T, 8, 1024>(a, st);
         return launch_odd_bwd_row<TY, T, 16, 1024>(a, st);
     }
-    const int V = a.d / E;
-    if (V <= 8) return launch_bwd_team<TY, T, E, 8, 1>(a, st);
-    if (V <= 16) return launch_bwd_team<TY, T, E, 16, 1>(a, st);
-    if (V <= 32) return launch_bwd_team<TY, T, E, 32, 1>(a, st);
-    if (V <= 64) return launch_bwd_team<TY, T, E, 32, 2>(a, st);
+    if (a.d <= 8 * E) return launch_bwd_team<TY, T, E, 8, 1>(a, st);
+    if (a.d <= 16 * E) return launch_bwd_team<TY, T, E, 16, 1>(a, st);
+    if (a.d <= 32 * E) return launch_bwd_team<TY, T, E, 32, 1>(a, st);
+    if (a.d <= 64 * E) return launch_bwd_team<TY, T, E, 32, 2>(a, st);
+    V = a.d / E;
     if (V <= 512) return launch_bwd_block<TY, T, E, 2, 256>(a, st);
     if (V <= 1024) return launch_bwd_block<TY, T, E, 2, 512>(a, st);
     if constexpr (sizeof(T) == 4) {
@@ -891,7 +927,7 @@ extern "C" dbc_status quantize_rows_i8(const void *x, int64_t x_stride, int dtyp
 
 extern "C" size_t rms_norm_backward_workspace(int64_t N, int64_t d) {
     if (N <= 0 || d <= 0) return 0;
-    return align_up((size_t)nm::bwd_lines(N, d) * (size_t)d * sizeof(float));
+    return align_up((size_t)nm::bwd_lines(N, d) * (size_t)d * sizeof(double));
 }
 
 extern "C" dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int dy_dtype, const void *s,
@@ -917,15 +953,16 @@ extern "C" dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int d
     if (dw && (!ws || !nm::aligned_to(ws, 16) || ws_bytes < rms_norm_backward_workspace(N, d)))
         return DBC_ERR_WORKSPACE;
     const nm::BwdArgs a{dy, s, ds, dx, {weight, w_dtype == DBC_BF16}, dy_stride, s_stride, ds_stride, dx_stride, N,
-                        (int)d, eps, 1.f / (float)d, dw ? static_cast<float *>(ws) : nullptr, dev_status};
+                        (int)d, eps, 1.f / (float)d, dw ? static_cast<double *>(ws) : nullptr, dev_status};
     using B = __nv_bfloat16;
     const bool by = dy_dtype == DBC_BF16, bs = dtype == DBC_BF16;
-    const int lines = by && bs ? nm::launch_bwd<B, B>(a, st)
-                      : by     ? nm::launch_bwd<B, float>(a, st)
-                      : bs     ? nm::launch_bwd<float, B>(a, st)
-                               : nm::launch_bwd<float, float>(a, st);
+    int V = 0;
+    const int lines = by && bs ? nm::launch_bwd<B, B>(a, V, st)
+                      : by     ? nm::launch_bwd<B, float>(a, V, st)
+                      : bs     ? nm::launch_bwd<float, B>(a, V, st)
+                               : nm::launch_bwd<float, float>(a, V, st);
     if (!lines) return DBC_ERR_CUDA;
-    if (dw) nm::dw_kernel<<<(unsigned)((d + 7) / 8), 1024, 0, st>>>(a.part, lines, (int)d, dw);
+    if (dw) nm::dw_kernel<<<(unsigned)((d + 7) / 8), 1024, 0, st>>>(a.part, lines, (int)d, V, dw);
     count_launches(dw ? 2 : 1);
     return launch_status();
 }

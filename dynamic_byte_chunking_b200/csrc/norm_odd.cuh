@@ -357,14 +357,17 @@ __global__ void __launch_bounds__(MAXT) odd_kernel(const FwdArgs a, int slot, in
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Backward, narrow rows: tiles of R rows, W lanes to a row.  Buffers: dy, s (and
-// ds) for two tiles, then dx; a lane keeps the dw sums of its NV columns, the CTA
-// joins them at the end (a fixed order).
+// Backward, narrow rows: tiles of R rows, W lanes to a row.  Buffers: the lanes' fp64
+// dw sums, then dy, s (and ds) for two tiles, then dx; a lane keeps the dw sums of
+// its NV columns, the CTA joins them at the end (a fixed order).
 template <class TY, class T, bool DW, int W, int NV>
-__global__ void __launch_bounds__(kThreads) odd_bwd_tile_kernel(const BwdArgs a, int R, int yslot, int slot) {
-    extern __shared__ __align__(16) char smem[];
+__global__ void __launch_bounds__(kThreads, 2) odd_bwd_tile_kernel(const BwdArgs a, int R, int yslot, int slot) {
+    extern __shared__ __align__(16) char all[];
     constexpr int TEAMS = kThreads / W;
-    const int t = threadIdx.x % W, team = threadIdx.x / W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = threadIdx.x % W, team = threadIdx.x / W;
+    double *const sums = reinterpret_cast<double *>(all);     // column j's at sums[j * kThreads + thread]
+    const int nj = (a.d + W - 1) / W;                         // a lane's columns
+    char *const smem = all + (DW ? nj * kThreads * (int)sizeof(double) : 0);
     const TY *const Y = static_cast<const TY *>(a.dy);
     const T *const S = static_cast<const T *>(a.s);
     const T *const D = static_cast<const T *>(a.ds);
@@ -378,7 +381,17 @@ __global__ void __launch_bounds__(kThreads) odd_bwd_tile_kernel(const BwdArgs a,
         if (j * W + t < a.d) a.w.get<1>(j * W + t, o);
         w[j] = o[0];
         acc[j] = 0.f;
+        if (DW && j < nj) sums[j * kThreads + threadIdx.x] = 0;
     }
+    auto fold = [&] {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (j < nj) sums[j * kThreads + threadIdx.x] += acc[j];
+            acc[j] = 0.f;
+        }
+    };
+    const int passes = R / TEAMS;                             // rows of a team in a tile, at most kFold
+    int done = 0;                                             // rows since the fold before
     const int64_t tiles = (a.N + R - 1) / R;
     auto start = [&](int64_t i, int st) {
         if (i < tiles) {
@@ -453,23 +466,21 @@ __global__ void __launch_bounds__(kThreads) odd_bwd_tile_kernel(const BwdArgs a,
             }
         }
         __syncthreads();
+        if (DW && (done += passes) > kFold - passes) {
+            fold();
+            done = 0;
+        }
         tile_out(X + r0 * a.xs, a.xs, obuf, slot, rows, a.d);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if constexpr (DW) {
-        __shared__ float line[kThreads / 32][W * NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float v = acc[j];
-#pragma unroll
-            for (int o = W; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane < W) line[warp][j * W + t] = v;
-        }
+        fold();
         __syncthreads();
         for (int c = threadIdx.x; c < a.d; c += kThreads) {
-            float v = 0.f;
+            const double *const at = sums + c / W * kThreads + c % W;
+            double v = 0;
 #pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) v += line[i][c];
+            for (int i = 0; i < TEAMS; ++i) v += at[i * W];
             a.part[(int64_t)blockIdx.x * a.d + c] = v;
         }
     }
@@ -477,9 +488,9 @@ __global__ void __launch_bounds__(kThreads) odd_bwd_tile_kernel(const BwdArgs a,
 
 // Backward, wide rows: one row per CTA at a time.  Slots: dy, s (and ds) for
 // `stages` rows; dx goes back into s's slot.  dw sums stay with the threads that
-// own the columns.
+// own the columns: in fp64 behind the slots or, where those leave no room (NV = 16), in the CTA's line.
 template <class TY, class T, bool DW, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) odd_bwd_kernel(const BwdArgs a, int yslot, int slot, int stages) {
+__global__ void __launch_bounds__(MAXT, MAXT > 512 ? 1 : 3) odd_bwd_kernel(const BwdArgs a, int yslot, int slot, int stages) {
     extern __shared__ __align__(16) char smem[];
     __shared__ float2 sh[32];
     __shared__ double2 shw[32];
@@ -505,73 +516,90 @@ __global__ void __launch_bounds__(MAXT) odd_bwd_kernel(const BwdArgs a, int yslo
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    constexpr bool OWN = DW && NV <= 8;
+    double *const sums = reinterpret_cast<double *>(smem + stages * stage);
+    double *const line = DW ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
     const int ahead = stages - 1;
     int st = 0;
     if (ahead) start(blockIdx.x, 0);
-    for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
-        __syncthreads();                              // the row before has left its slots
-        if (ahead) start(r + gridDim.x, st ^ 1);
-        else start(r, 0);
-        copies_done(ahead);
-        __syncthreads();
-        char *const in = smem + st * stage;
-        const TY *const dy = reinterpret_cast<const TY *>(in + off16(Y + r * a.ys));
-        const T *const s = reinterpret_cast<const T *>(in + yslot + off16(S + r * a.ss));
-        const T *const ds = reinterpret_cast<const T *>(in + yslot + slot + (D ? off16(D + r * a.ds_s) : 0));
-        float y[NV], f[NV];
-        float2 p = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = j * W + t;
-            y[j] = c < a.d ? ld_f(dy + c) : 0.f;
-            f[j] = c < a.d ? ld_f(s + c) : 0.f;
-            p.x = fmaf(f[j], f[j], p.x);
-            p.y = fmaf(y[j] * w[j], f[j], p.y);
-        }
-        p = team_pair(p, Add(), Add(), sh);       // (its barrier: everybody has read s)
-        BwdFactor k(p.x, p.y, a);
-        bool odd = !in_range(p.x, p.y);                  // the same in the whole team
-        if (faint(p.y)) {
-            bool some = false;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) some |= y[j] * w[j] != 0.f;
-            odd |= __syncthreads_or(some) != 0;
-        }
-        if (odd) {
-            double2 q = make_double2(0, 0);
+    bool first = true;
+    for (int64_t r = blockIdx.x; r < a.N; first = false) {
+        // kFold rows at a time (all of them where no dw is wanted), then the fold
+        const int64_t end = DW ? min(a.N, r + kFold * (int64_t)gridDim.x) : a.N;
+        for (; r < end; r += gridDim.x) {
+            __syncthreads();                              // the row before has left its slots
+            if (ahead) start(r + gridDim.x, st ^ 1);
+            else start(r, 0);
+            copies_done(ahead);
+            __syncthreads();
+            char *const in = smem + st * stage;
+            const TY *const dy = reinterpret_cast<const TY *>(in + off16(Y + r * a.ys));
+            const T *const s = reinterpret_cast<const T *>(in + yslot + off16(S + r * a.ss));
+            const T *const ds = reinterpret_cast<const T *>(in + yslot + slot + (D ? off16(D + r * a.ds_s) : 0));
+            float y[NV], f[NV];
+            float2 p = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                q.x += (double)f[j] * f[j];
-                q.y += (double)(y[j] * w[j]) * f[j];
+                const int c = j * W + t;
+                y[j] = c < a.d ? ld_f(dy + c) : 0.f;
+                f[j] = c < a.d ? ld_f(s + c) : 0.f;
+                p.x = fmaf(f[j], f[j], p.x);
+                p.y = fmaf(y[j] * w[j], f[j], p.y);
             }
-            q = team_pair(q, Add(), Add(), shw);
-            k = BwdFactor(q.x, q.y, a);
-            if (t == 0 && (!isfinite(q.x) || !isfinite(q.y))) flag(a.st, DBC_ERR_NONFINITE);
-        }
-        T *const dx = static_cast<T *>(a.dx) + r * a.xs;
-        T *const o = reinterpret_cast<T *>(in + yslot + off16(dx));
+            p = team_pair(p, Add(), Add(), sh);       // (its barrier: everybody has read s)
+            BwdFactor k(p.x, p.y, a);
+            bool odd = !in_range(p.x, p.y);                  // the same in the whole team
+            if (faint(p.y)) {
+                bool some = false;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = j * W + t;
-            const float xh = f[j] * k.k.pre * k.k.rstd;
-            if (DW) acc[j] = fmaf(y[j], xh, acc[j]);
-            if (c < a.d) {
-                float u[1] = {fmaf(-xh, k.c, y[j] * w[j]) * k.k.rstd * k.k.pre};
-                if (D) u[0] += ld_f(ds + c);
-                Frag<T, 1> q;
-                q.set(u);
-                q.store(o + c);
+                for (int j = 0; j < NV; ++j) some |= y[j] * w[j] != 0.f;
+                odd |= __syncthreads_or(some) != 0;
+            }
+            if (odd) {
+                double2 q = make_double2(0, 0);
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    q.x += (double)f[j] * f[j];
+                    q.y += (double)(y[j] * w[j]) * f[j];
+                }
+                q = team_pair(q, Add(), Add(), shw);
+                k = BwdFactor(q.x, q.y, a);
+                if (t == 0 && (!isfinite(q.x) || !isfinite(q.y))) flag(a.st, DBC_ERR_NONFINITE);
+            }
+            T *const dx = static_cast<T *>(a.dx) + r * a.xs;
+            T *const o = reinterpret_cast<T *>(in + yslot + off16(dx));
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = j * W + t;
+                const float xh = f[j] * k.k.pre * k.k.rstd;
+                if (DW) acc[j] = fmaf(y[j], xh, acc[j]);
+                if (c < a.d) {
+                    float u[1] = {fmaf(-xh, k.c, y[j] * w[j]) * k.k.rstd * k.k.pre};
+                    if (D) u[0] += ld_f(ds + c);
+                    Frag<T, 1> q;
+                    q.set(u);
+                    q.store(o + c);
+                }
+            }
+            __syncthreads();
+            row_out(dx, in + yslot, a.d, t, W);
+            if (ahead) st ^= 1;
+        }
+        if (DW) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float one[1] = {acc[j]};
+                if (OWN) fold_sums<1, false>(sums + j * W + t, 0, one, first);
+                else if (j * W + t < a.d) fold_sums<1, true>(line + j * W + t, 0, one, first);
+                acc[j] = 0.f;
             }
         }
-        __syncthreads();
-        row_out(dx, in + yslot, a.d, t, W);
-        if (ahead) st ^= 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if constexpr (DW) {
+    if (OWN) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (j * W + t < a.d) a.part[(int64_t)blockIdx.x * a.d + j * W + t] = acc[j];
+            if (j * W + t < a.d) line[j * W + t] = sums[j * W + t];
     }
 }
 

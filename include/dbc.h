@@ -469,7 +469,8 @@ DBC_API dbc_status quantize_rows_i8(const void *x, int64_t x_stride, int dtype, 
  * dw       out fp32 [d] (overwritten), or NULL when it is not needed.
  * ws       workspace of rms_norm_backward_workspace(N, d) bytes; not read when
  *          dw is NULL.  Calls that can overlap need workspaces of their own.
- * dw is summed in a fixed order: repeated calls agree bitwise.
+ * dw is summed in a fixed order (up to 16 rows in fp32, those sums in fp64):
+ * repeated calls agree bitwise.
  * Limits and errors as in rms_norm, and WORKSPACE; NONFINITE is flagged for
  * rows whose dy w or s is not finite.
  * ------------------------------------------------------------------------- */

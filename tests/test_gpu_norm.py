@@ -534,3 +534,30 @@ def test_gradients_whose_products_leave_fp32(T, d):
         _close(dx, rx, bx + rs * 2.0 ** -150 * (2 + np.abs(s * rs)), f"dx eps={eps}")
         _close(dw, rw, bw, f"dw eps={eps}")
     assert st.item() == 0
+
+
+@pytest.mark.parametrize("TY,T,d,N", [("bf16", "bf16", 64, 600_000), ("f32", "bf16", 256, 160_000), ("bf16", "bf16", 512, 100_000),
+                                      ("bf16", "bf16", 1536, 40_000), ("f32", "f32", 1536, 40_000), ("bf16", "f32", 4096, 20_000),
+                                      ("bf16", "bf16", 8192, 10_000), ("f32", "bf16", 16384, 5_000), ("f32", "f32", 12000, 5_000),
+                                      ("bf16", "bf16", 33, 2_000_000), ("bf16", "f32", 77, 600_000),
+                                      ("f32", "bf16", 257, 310_000), ("bf16", "bf16", 500, 160_000), ("f32", "f32", 1531, 40_000),
+                                      ("bf16", "bf16", 5001, 10_000), ("bf16", "f32", 9001, 5_000)])
+def test_dw_of_many_rows_keeps_small_terms(TY, T, d, N):
+    """dw where every column's terms are 1 in the first 1/64 of the rows and less than half a step of fp32 at 1 in
+    the others: one fp32 chain over a thread's rows loses all of those, 63 roundings of the result (half of it where
+    only every other thread has such rows in front).
+
+    Rows of +-1 have one rstd, off by half a rounding of 1/d, half of the mean and two steps (four roundings) of
+    rsqrtf; the products with it round once, sixteen of them add up in fp32 (15 roundings, all terms are positive)
+    before they join fp64 sums, and so does the result: 22 in all, and one for the fp64 additions."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}
+    g = torch.Generator(device="cuda").manual_seed(d)
+    s = torch.randint(0, 2, (N, d), generator=g, device="cuda", dtype=torch.int8).mul_(2).sub_(1)
+    first, small = N // 64, 255 * 2.0 ** -32
+    dy = s.to(dt[TY])
+    dy[first:] *= small
+    _, dw = dbc.rms_norm_backward(dy, s.to(dt[T]), None, eps=1e-30)
+    ref = np.full(d, first + (N - first) * small)
+    _close(dw, ref, ref * 23 * o.U32, "dw")
