@@ -50,6 +50,15 @@ __device__ __forceinline__ float bias_at(const Args &p, int64_t j) {
                        : static_cast<const float *>(p.bias)[j];
 }
 
+// sum * a_scale * b_scale (+ bias).  The smaller scale comes first: 2^31 times it overflows only where the result
+// does, and its product with a whole number keeps fp32's precision at any size.
+__device__ __forceinline__ float scaled(float sum, float as, float bs, float bias) {
+    const bool a = fabsf(as) < fabsf(bs);
+    return fmaf(sum * (a ? as : bs), a ? bs : as, bias);
+}
+// Up to this the token's scale may come first whatever the other is.
+constexpr float kBigScale = 0x1p96f;
+
 // The four (at the end of the depth: fewer) K steps of one stage.
 __device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sa, uint32_t sb, uint32_t idesc, int left, bool first) {
     const uint64_t da = tc::sdesc(sa, 16, 1024), db = tc::sdesc(sb, 16, 1024);
@@ -265,6 +274,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_at(release[b]);
             if (n0 >= p.N || r0 >= p.M) continue;
+            if (__any_sync(0xffffffffu, fmaxf(fmaxf(fabsf(ra[0]), fabsf(ra[1])), fmaxf(fabsf(ra[2]), fabsf(ra[3]))) > kBigScale)) {
+                // a scale that may have to come second: the sums go through the staging, element by element
+                // (the order chosen in the loop below would cost every call 4 to 6 %)
+#pragma unroll
+                for (int c0 = 0; c0 < 64; c0 += 16) {
+                    if (TMA_OUT && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int i = c0 / 8; i < c0 / 8 + 2; ++i)
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            *reinterpret_cast<uint2 *>(slab + ((lane >> 2) + h * 8) * 64 + (i & 1) * 32 + (lane & 3) * 8) =
+                                make_uint2(v[h >> 1][i * 4 + (h & 1) * 2], v[h >> 1][i * 4 + (h & 1) * 2 + 1]);
+                    __syncwarp();
+                    const int j = n0 + c0 + lane % 16, rows = min(32, p.M - r0);
+                    for (int r = lane / 16; r < rows && j < p.N; r += 2) {
+                        const int sum = *reinterpret_cast<const int *>(slab + r * 64 + lane % 16 * 4);
+                        const float o = scaled((float)sum, p.as[r0 + r], p.bs[j], BIAS ? bias_at(p, j) : 0.f);
+                        const int64_t at = (int64_t)(r0 + r) * p.ldo + j;
+                        if constexpr (BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(o);
+                        else static_cast<float *>(p.out)[at] = o;
+                    }
+                }
+                continue;
+            }
 #pragma unroll
             for (int c0 = 0; c0 < 64; c0 += COLS) {
                 if (TMA_OUT && lane == 0)                // the store before has read the staging
@@ -418,9 +452,10 @@ __global__ void __launch_bounds__(128)
         }
     }
     const int rows = min(BT, p.M - m0);
-    if (tid < BT) s_as[tid] = tid < rows ? p.as[m0 + tid] : 0.f;
+    const float my_as = tid < rows ? p.as[m0 + tid] : 0.f;
+    if (tid < BT) s_as[tid] = my_as;
     tc::fence_before_sync();
-    __syncthreads();
+    const bool order = __syncthreads_or(fabsf(my_as) > kBigScale) != 0;
     tc::fence_after_sync();
     const uint32_t tbase = tmem_base;
 
@@ -474,7 +509,7 @@ __global__ void __launch_bounds__(128)
     tc::fence_after_sync();
     const bool ok = s_ok != 0;
     auto put = [&](int m, int n, int sum, float as, float bs, float bias) {
-        const float v = fmaf((float)sum * as, bs, bias);
+        const float v = order ? scaled((float)sum, as, bs, bias) : fmaf((float)sum * as, bs, bias);
         const int64_t at = (int64_t)(m0 + m) * p.ldo + n;
         if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
         else static_cast<float *>(p.out)[at] = v;
@@ -491,6 +526,10 @@ __global__ void __launch_bounds__(128)
                 float f[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) f[j] = fmaf((p.K ? (float)(int)v[j] : 0.f) * s_as[c0 + j], bs, bias);
+                if (order) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[j] = scaled(p.K ? (float)(int)v[j] : 0.f, s_as[c0 + j], bs, bias);
+                }
 #pragma unroll
                 for (int j = 0; j < 16; ++j, o += p.ldo)
                     if (c0 + j < rows && n < p.N) store_one(o, f[j]);

@@ -485,7 +485,8 @@ DBC_API dbc_status rms_norm_backward(const void *dy, int64_t dy_stride, int dy_d
  * matmul_i8 -- product of 8-bit integers with token and channel scales.
  *
  *   out[i, j] = T(a_scale[i] * b_scale[j] * sum_k a[i, k] b[j, k] (+ bias[j])),
- * the sum exact in 32-bit integers, the rest in fp32, rounded once.
+ * the sum exact in 32-bit integers, the rest in fp32 (in an order that leaves
+ * fp32's range only where the result does), rounded once.
  *
  * a        int8 [M, K], row i at a + i * lda; b int8 [N, K], row j (an output
  *          channel) at b + j * ldb.  lda, ldb multiples of 16, >= K, both bases

@@ -239,3 +239,30 @@ def test_chunk_path_in_8_bits(rows, T, d, d_g):
     ref2 = o.rms_norm(s2.double().cpu().numpy(), wn, 1e-6)
     assert np.all(np.abs(y2.double().cpu().numpy() - ref2) <= o.rms_norm_bound(ref2, "bf16"))
     assert st.item() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 40, 512), (70, 300, 64), (16, 300, 2048), (200, 256, 4096), (1500, 1536, 256)])
+def test_scales_far_from_one(M, N, K):
+    """Results inside fp32's range from scales whose product with the sum alone is not: the largest with sums of 2^22
+    and more, the smallest (subnormal) with the largest."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    rng = np.random.default_rng(M)
+    a, at = _operand(rng, M, K)
+    b, bt = _operand(rng, N, K)
+    a[::2], b[::2] = 127, 127
+    at.copy_(torch.from_numpy(a)), bt.copy_(torch.from_numpy(b))
+    ea = np.where(np.arange(M) % 3 == 0, 120, np.where(np.arange(M) % 3 == 1, -135, 3))
+    for eb in (-110, 0, 100):
+        sa = (rng.uniform(1, 2, M) * 2.0 ** ea).astype(np.float32)
+        sb = (rng.uniform(1, 2, N) * 2.0 ** eb).astype(np.float32)
+        for bias in (None, "f32"):
+            bv = None if bias is None else o.store(rng.standard_normal(N).astype(np.float32), "f32")
+            out = dbc.matmul_i8(at, torch.from_numpy(sa).cuda(), bt, torch.from_numpy(sb).cuda(), out_dtype=torch.float32,
+                                bias=None if bv is None else torch.from_numpy(bv).float().cuda())
+            ref = o.matmul_i8(a, sa.astype(np.float64), b, sb.astype(np.float64), bv)
+            g = out.double().cpu().numpy()
+            keep = np.abs(ref) < 2.0 ** 127
+            bound = o.matmul_i8_bound(ref, bv, "f32") + o.TINY["f32"]
+            assert np.all(np.abs(g - ref)[keep] <= bound[keep]), (eb, bias)
+            assert np.all(np.isinf(g[np.abs(ref) > 2.0 ** 128 * (1 + 2.0 ** -20)]))
