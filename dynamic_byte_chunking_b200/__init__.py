@@ -620,7 +620,7 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, residual=None, out_dtype=None
              stream=None):
     """(y, s): s = x + residual rounded to x's dtype (None without a residual) and y = s / rms(s) * weight
     in ``out_dtype`` (x's by default), over the last dimension of x [..., d] (fp32 or bf16; weight [d] fp32 or
-    bf16, or None for ones).  ``s`` may be x or residual themselves, ``y`` may be x: updated in place."""
+    bf16, or None for ones).  ``s`` may be x or residual themselves, ``y`` may be x when ``s`` is not: updated in place."""
     torch = _torch()
     to = _elsewhere(stream, x, weight, residual, y, s, dev_status)
     if to is not None:

@@ -893,7 +893,7 @@ extern "C" dbc_status rms_norm(const void *x, int64_t x_stride, int dtype, const
     if (!nm::known(y_dtype)) return DBC_ERR_UNSUPPORTED;
     if (y_stride < d) return DBC_ERR_INVALID_ARG;
     if (N == 0) return DBC_OK;
-    if (!y || !nm::aligned_to(y, nm::esize(y_dtype))) return DBC_ERR_INVALID_ARG;
+    if (!y || y == s || !nm::aligned_to(y, nm::esize(y_dtype))) return DBC_ERR_INVALID_ARG;
     return nm::launch_fwd<nm::kPlain>(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -404,9 +404,10 @@ DBC_API dbc_status hnet_route(const void *H, const int64_t *offsets, int64_t row
  * weight   NULL (ones) or [d], fp32 or bf16 (w_dtype).
  * s        out [N, d] of x's type, s_stride; NULL when the sum is not needed;
  *          must be NULL without residual.  May be x or residual themselves.
- * y        out [N, d] fp32 or bf16 (y_dtype), y_stride.  May be x itself, and
- *          residual when s is neither, given equal types and strides.  Other
- *          overlaps of inputs and outputs are not allowed.
+ * y        out [N, d] fp32 or bf16 (y_dtype), y_stride.  May be x itself unless
+ *          s is, and residual when s is neither, given equal types and strides
+ *          (y == s is refused).  Other overlaps of inputs and outputs are not
+ *          allowed.
  * All strides are in elements, >= d.  Any d from 1 to 16384; quickest where
  * every row starts on a 16-byte boundary and holds a multiple of 16 bytes.
  * A row with a NaN gives NaN, one with an infinity 0 and NaN at the infinity;

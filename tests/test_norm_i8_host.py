@@ -96,3 +96,11 @@ def test_binding_takes_cuda_tensors_only():
                  lambda: dbc.rms_norm_backward(x, x), lambda: dbc.matmul_i8(c, one, c, one)):
         with pytest.raises(ValueError, match="CUDA tensors only"):
             call()
+
+
+def test_one_buffer_for_both_outputs_is_refused(L):
+    """y over s would leave the sum nowhere; y over x with s over the residual is the in-place form."""
+    Q = ctypes.c_void_p(8192)
+    assert _norm(L, r=Q, rs=64, s=P, ss=64, y=P) == 1
+    assert _norm(L, r=Q, rs=64, s=Q, ss=64, y=Q) == 1
+    assert _norm(L, r=Q, rs=64, s=Q, ss=64, y=P, N=0) == 0
