@@ -343,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
                             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         }
                     } else {
-                        // output rows off the 16-byte grid: element by element, row after row of the slab
+                        // output rows or widths off the 16-byte grid: element by element, row after row of the slab
                         __syncwarp();
                         const int cols = min(COLS, p.N - n0 - c0), rows = min(32, p.M - r0);
                         constexpr int STEP = 32 / COLS;  // rows at a time
@@ -616,7 +616,8 @@ dbc_status launch_wide(const int8_t *a, int64_t lda, const int8_t *b, int64_t ld
     if (!tma::encode_i8_rows(&ta, a, p.M, p.K, lda, 128) || !tma::encode_i8_rows(&tb, b, p.N, p.K, ldb, 128))
         return DBC_ERR_CUDA;
     const int64_t esz = p.out_bf16 ? 2 : 4;
-    const bool tma_out = aligned16(p.out) && p.ldo * esz % 16 == 0 &&
+    // (a tile store writes whole 16-byte pieces: with a width that ends inside one it would write behind the row)
+    const bool tma_out = aligned16(p.out) && p.ldo * esz % 16 == 0 && p.N * esz % 16 == 0 &&
                          tma::encode_out_rows(&to, p.out, p.out_bf16, p.M, p.N, p.ldo, 32);
     using K = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Args);
     static const K kernels[8] = {wide_kernel<false, false, false>, wide_kernel<false, false, true>,

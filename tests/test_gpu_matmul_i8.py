@@ -266,3 +266,28 @@ def test_scales_far_from_one(M, N, K):
             bound = o.matmul_i8_bound(ref, bv, "f32") + o.TINY["f32"]
             assert np.all(np.abs(g - ref)[keep] <= bound[keep]), (eb, bias)
             assert np.all(np.isinf(g[np.abs(ref) > 2.0 ** 128 * (1 + 2.0 ** -20)]))
+
+
+# From M > 128 and 24 tiles of 256 x 256 on the wide kernel runs, below it the split one.
+@pytest.mark.parametrize("bias", [None, "bf16", "f32"])
+@pytest.mark.parametrize("T", ["bf16", "f32"])
+def test_wide_kernel(T, bias):
+    """6 x 6 tiles with ragged edges; outputs packed, and inside wider buffers on (tile stores) and off the 16-byte
+    grid (element stores; a width that ends inside 16 bytes among them), whose guards stay; depths shorter than a
+    step and ending inside one."""
+    import torch
+    rng = np.random.default_rng(7)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dt = torch.bfloat16 if T == "bf16" else torch.float32
+    M = 1300
+    for N, ld, c0 in [(1283, None, 0), (1288, None, 0), (1283, 1304, 8), (1288, 1304, 8), (1300, 1312, 8),
+                      (1288, 1297, 3)]:
+        for K in (1, 17, 33, 129, 777):
+            if ld is None:
+                _case(rng, M, N, K, T, bias, st=st)
+                continue
+            buf = torch.full((M + 2, ld), 5.0, dtype=dt, device="cuda")
+            _case(rng, M, N, K, T, bias, out=buf[1:M + 1, c0:c0 + N], st=st)
+            buf[1:M + 1, c0:c0 + N] = 5.0
+            assert bool((buf == 5.0).all())
+    assert st.item() == 0
