@@ -291,3 +291,67 @@ def test_wide_kernel(T, bias):
             buf[1:M + 1, c0:c0 + N] = 5.0
             assert bool((buf == 5.0).all())
     assert st.item() == 0
+
+
+# tiles of 128 tokens, depth not split and split in two (20 and 18 wide tiles); tiles of 64 and 32 tokens with the
+# depth in 4 and 2; both sides of the switch to the wide kernel (23 and 24 tiles) with a deep product
+@pytest.mark.parametrize("M,N,K", [(1280, 1000, 100), (600, 1536, 777), (300, 1000, 2000), (260, 1000, 1100), (5888, 256, 2048),
+                                   (5889, 256, 2048), (130, 5888, 1500), (257, 3100, 1500)])
+@pytest.mark.parametrize("T,bias", [("f32", "bf16"), ("bf16", "f32"), ("f32", None)])
+def test_split_kernel_and_the_switch(M, N, K, T, bias):
+    import torch
+    rng = np.random.default_rng(M + K)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _case(rng, M, N, K, T, bias, st=st)
+    assert st.item() == 0
+
+
+def test_wide_kernel_largest_sums():
+    """Sums of 2^31 - 16384, and a NaN scale that reaches its row (or channel) only."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    K, M, N = 131071, 1300, 1283
+    a = torch.full((M, K + 1), -128, dtype=torch.int8, device="cuda")[:, :K]
+    b = torch.full((N, K + 1), -128, dtype=torch.int8, device="cuda")[:, :K]
+    b[1] = 127
+    sa, sb = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    out = dbc.matmul_i8(a, sa, b, sb, out_dtype=torch.float32)
+    assert bool((out[:, 1] == float(np.float32(-131071 * 16256))).all())
+    out[:, 1] = out[0, 0]
+    assert bool((out == float(np.float32(131071 * 16384))).all())
+    sa[700], sb[600] = float("nan"), float("nan")
+    out = dbc.matmul_i8(a, sa, b, sb, out_dtype=torch.float32)
+    assert bool(out[700].isnan().all()) and bool(out[:, 600].isnan().all())
+    out[700], out[:, 600] = 0, 0
+    assert not bool(out.isnan().any())
+
+
+def test_wide_kernel_on_two_streams_and_in_graphs():
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    torch.manual_seed(3)
+    M, N, K = 1500, 1536, 256
+    b = torch.randint(-127, 128, (N, K), device="cuda", dtype=torch.int8)
+    sb = torch.rand(N, device="cuda")
+    graphs = []
+    for _ in range(2):
+        side = torch.cuda.Stream()
+        a, sa = torch.zeros(M, K, dtype=torch.int8, device="cuda"), torch.rand(M, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            out = dbc.matmul_i8(a, sa, b, sb, out_dtype=torch.float32)
+        graphs.append((g, a, sa, out, side))
+    for _ in range(3):
+        data = [torch.randint(-127, 128, (M, K), device="cuda", dtype=torch.int8) for _ in graphs]
+        torch.cuda.synchronize()
+        for (g, a, sa, out, side), v in zip(graphs, data):
+            with torch.cuda.stream(side):
+                a.copy_(v)
+                g.replay()
+                eager = dbc.matmul_i8(a, sa, b, sb, out_dtype=torch.float32)
+            side.synchronize()
+            assert torch.equal(out, eager)
+        for (g, a, sa, out, side), v in zip(graphs, data):
+            ref = (v.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
+            assert torch.all((out.double() - ref).abs() <= ref.abs() * 4 * o.U32)

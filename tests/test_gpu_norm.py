@@ -561,3 +561,72 @@ def test_dw_of_many_rows_keeps_small_terms(TY, T, d, N):
     _, dw = dbc.rms_norm_backward(dy, s.to(dt[T]), None, eps=1e-30)
     ref = np.full(d, first + (N - first) * small)
     _close(dw, ref, ref * 23 * o.U32, "dw")
+
+
+@pytest.mark.parametrize("N,d", [(200003, 33), (100003, 131), (60001, 257), (20011, 777), (5003, 1531), (3001, 3333)])
+def test_many_odd_rows(N, d):
+    """Rows off the 16-byte grid, several tiles (or rows) to a CTA and several rows of a tile to a team: against the
+    oracle, packed, inside wider buffers and in place."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    rng = np.random.default_rng(N)
+    st = _status()
+    x, r, dy, ds = (_vals(rng, (N, d), "bf16") for _ in range(4))
+    w = _weight(rng, d, "bf16")
+    xt, rt, dyt, dst, wt = (_t(v, "bf16") for v in (x, r, dy, ds, w))
+    s = o.residual_sum(x, r, "bf16")
+    ref = o.rms_norm(s, w, EPS)
+    by = o.rms_norm_bound(ref, "bf16")
+
+    def wider(t=None, dtype=torch.bfloat16):
+        buf = torch.full((N, d + 4), 7, dtype=dtype, device="cuda")
+        if t is not None:
+            buf[:, 1:d + 1] = t
+        return buf
+
+    def kept(buf):
+        return bool((buf[:, 0] == 7).all() and (buf[:, d + 1:] == 7).all())
+
+    y, sg = dbc.rms_norm(xt, wt, eps=EPS, residual=rt, dev_status=st)
+    _close(y, ref, by, "y")
+    assert np.array_equal(_np(sg), s)
+    yb, sb = wider(), wider()
+    dbc.rms_norm(wider(xt)[:, 1:d + 1], wt, eps=EPS, residual=wider(rt)[:, 1:d + 1], y=yb[:, 1:d + 1], s=sb[:, 1:d + 1])
+    _close(yb[:, 1:d + 1], ref, by, "strided y")
+    assert torch.equal(sb[:, 1:d + 1], sg) and kept(yb) and kept(sb)
+    x2, r2 = xt.clone(), rt.clone()
+    dbc.rms_norm(x2, wt, eps=EPS, residual=r2, y=x2, s=r2)
+    assert torch.equal(x2, y) and torch.equal(r2, sg)
+
+    qr, sr = o.rms_norm_i8(s, w, EPS)
+    q, sc, _ = dbc.rms_norm_i8(xt, wt, eps=EPS, residual=rt, dev_status=st)
+    assert np.array_equal(q.cpu().numpy(), qr)
+    _close(sc, sr, np.abs(sr) * (o.CHAIN / 2 + o.OPS) * o.U32, "scale")
+    qb = wider(dtype=torch.int8)
+    dbc.rms_norm_i8(wider(xt)[:, 1:d + 1], wt, eps=EPS, residual=rt, q=qb[:, 1:d + 1])
+    assert torch.equal(qb[:, 1:d + 1], q) and kept(qb)
+    r3 = rt.clone()
+    q3, _, _ = dbc.rms_norm_i8(xt, wt, eps=EPS, residual=r3, s=r3, q=torch.empty(N, d, dtype=torch.int8, device="cuda"))
+    assert torch.equal(q3, q) and torch.equal(r3, sg)
+    qr, sr = o.quantize_rows_i8(x)
+    q, sc = dbc.quantize_rows_i8(xt, dev_status=st)
+    assert np.array_equal(q.cpu().numpy(), qr)
+    _close(sc, sr, np.abs(sr) * 2 * o.U32, "quantize scale")
+    del qr, sr, ref, by
+
+    rx, rw = o.rms_norm_backward(dy, s, w, EPS, ds)
+    bx, bw = o.backward_bounds(dy, s, w, EPS, ds, "bf16")
+    dx, dw = dbc.rms_norm_backward(dyt, sg, wt, eps=EPS, dsum=dst, dev_status=st)
+    _close(dx, rx, bx, "dx")
+    _close(dw, rw, bw, "dw")
+    xb = wider()
+    _, dw2 = dbc.rms_norm_backward(wider(dyt)[:, 1:d + 1], sb[:, 1:d + 1], wt, eps=EPS, dsum=wider(dst)[:, 1:d + 1],
+                                   dx=xb[:, 1:d + 1])
+    _close(xb[:, 1:d + 1], rx, bx, "strided dx")
+    _close(dw2, rw, bw, "strided dw")
+    assert kept(xb)
+    for k in range(3):
+        c = [dyt.clone(), sg.clone(), dst.clone()]
+        _, dw2 = dbc.rms_norm_backward(c[0], c[1], wt, eps=EPS, dsum=c[2], dx=c[k])
+        assert torch.equal(c[k], dx) and torch.equal(dw2, dw)
+    assert st.item() == 0
