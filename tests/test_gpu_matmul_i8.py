@@ -355,3 +355,18 @@ def test_wide_kernel_on_two_streams_and_in_graphs():
         for (g, a, sa, out, side), v in zip(graphs, data):
             ref = (v.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
             assert torch.all((out.double() - ref).abs() <= ref.abs() * 4 * o.U32)
+
+
+@pytest.mark.parametrize("N", [16400, 16401])
+def test_outputs_past_32_bits(N):
+    """More than 2^31 outputs (tile and element stores): the last rows as a call of their own gives them."""
+    import dynamic_byte_chunking_b200 as dbc
+    import torch
+    torch.manual_seed(N)
+    M, K = 140_000, 32
+    a = torch.randint(-127, 128, (M, K), device="cuda", dtype=torch.int8)
+    b = torch.randint(-127, 128, (N, K), device="cuda", dtype=torch.int8)
+    sa, sb = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    out = dbc.matmul_i8(a, sa, b, sb)
+    for r in (slice(0, 40), slice(131_000, 131_040), slice(M - 40, M)):
+        assert torch.equal(out[r], dbc.matmul_i8(a[r], sa[r], b, sb))
