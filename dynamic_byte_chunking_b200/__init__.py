@@ -620,7 +620,9 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, residual=None, out_dtype=None
              stream=None):
     """(y, s): s = x + residual rounded to x's dtype (None without a residual) and y = s / rms(s) * weight
     in ``out_dtype`` (x's by default), over the last dimension of x [..., d] (fp32 or bf16; weight [d] fp32 or
-    bf16, or None for ones).  ``s`` may be x or residual themselves, ``y`` may be x when ``s`` is not: updated in place."""
+    bf16, or None for ones).  ``s`` may be x or residual themselves, ``y`` may be x when ``s`` is not: updated in place.
+    Inputs that are neither contiguous nor [N, d] with unit inner stride (a part of a wider [rows, T, D] buffer, for one)
+    are copied first, here and in the calls below; outputs have to be one of the two."""
     torch = _torch()
     to = _elsewhere(stream, x, weight, residual, y, s, dev_status)
     if to is not None:
@@ -783,8 +785,8 @@ def chunk_project_i8(H, idx, idx_offsets, weight, W_q, W_scale, *, rows: int, T:
                      total: Optional[int] = None, eps: float = 1e-6, bias=None, out_dtype=None, dev_status=None,
                      stream=None):
     """Chunk vectors to the global width in 8 bits: (Z, out) with Z = H[s_k] (:func:`chunk_gather`) and
-    out = bf16(rms_norm(Z, weight) W) through :func:`rms_norm_i8` and :func:`matmul_i8`.  ``W_q`` int8 [d_g, d]
-    and ``W_scale`` fp32 [d_g] come from ``quantize_rows_i8(W_proj.t())``, once."""
+    out = bf16(rms_norm(Z, weight) W) through :func:`rms_norm_i8` and :func:`matmul_i8` (weight None: the norm without
+    a weight).  ``W_q`` int8 [d_g, d] and ``W_scale`` fp32 [d_g] come from ``quantize_rows_i8(W_proj.t())``, once."""
     torch = _torch()
     to = _elsewhere(stream, H, idx, idx_offsets, weight, W_q, W_scale, offsets, bias, dev_status)
     if to is not None:

@@ -19,7 +19,8 @@
 // measured bf16 rate; the tensor pipe is fed without a pause: a stage of 512 cycles' MMAs every 541) and
 // 108 in long ones, where the power cap holds the clock near 1.45 GHz (torch._int_mm, without scales: 106);
 // 32768 x 1536 x 512 34 (outputs and their staging share the time with the loads: 28 without the stores,
-// 24 without the epilogue's arithmetic); 4 x 8192 x 8192 10.6 (98 % of HBM's copy rate).
+// 24 without the epilogue's arithmetic); 4 x 8192 x 8192 15.9 with the weight in HBM (66 % of the copy's
+// rate) and 10.7 with it in L2.
 // Every wait is bounded; a timeout flags DBC_ERR_TIMEOUT and the CTA skips its
 // remaining work, after waiting for its copies and MMAs in flight.
 #include <cuda.h>
@@ -583,8 +584,9 @@ dbc_status launch_split(const int8_t *a, int64_t lda, const int8_t *b, int64_t l
     const int nt = (p.N + 127) / 128, mt = (p.M + BT - 1) / BT, ks = (p.K + 127) / 128;
     int splits = 1;
     // At least two steps of depth to a CTA, and no more CTAs than run at once: one to an SM with 128
-    // tokens' stages (128 x 4096 x 4096 took 12 us with four splits, 25 with eight), else two (64 x 8192 x
-    // 8192 took 15.6 us with two to an SM, 22.3 with one).
+    // tokens' stages (200 x 4096 x 4096 takes 12.2 us so, 17.9 with up to two; 100 x 5000 x 5000 13.9 and
+    // 19.6), else two (64 x 8192 x 8192 takes 12.2 us with up to two to an SM, 15.3 with one; 4 x 8192 x 8192
+    // 10.7 and 13.1).
     while (splits < 8 && splits * 4 <= ks && (int64_t)nt * mt * splits * 2 <= 148 * (BT > 64 ? 1 : 2)) splits *= 2;
     if (cudaFuncSetAttribute(split_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) !=
         cudaSuccess) {
@@ -661,8 +663,13 @@ extern "C" dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_sca
     mi::Args p{a_scale, b_scale, bias, out, ldo, (int)M, (int)N, (int)K, bias_dtype == DBC_BF16,
                out_dtype == DBC_BF16, dev_status};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // 24 of the 74 pairs' tiles are where the wide kernel overtakes the split one (4096 x 512 x 512, 32
-    // tiles: 10.8 us against 14.2; 1000 x 1000 x 1000, 16 tiles: 13.7 against 9.1).
+    // From 24 of the 74 pairs' tiles on.  Where the split kernel needs a second wave (more than 148 of its
+    // tiles of 128 x 128) the wide one is ahead but for the shortest depths: 2048 x 2048 (64 wide tiles) takes
+    // 10.5, 12.2 and 19.5 us at depths 256, 1024 and 4096, split 10.2, 13.8 and 27.1; 3000 x 1024 (48) 10.4,
+    // 12.0 and 19.1, split 10.1, 13.4 and 26.8.  Below 24 it is behind: 1280 x 1024 (20) 10.3, 11.9 and 18.6,
+    // split 5.7, 7.4 and 14.4.  Between 24 and 37 tiles the split kernel, since its epilogue is short, would
+    // still be ahead (2048 x 1024, 32 tiles: 5.7, 7.6 and 14.6 against 10.3, 12.0 and 18.9; 4096 x 512 x 512:
+    // 6.2 against 10.7).
     const int64_t wide_tiles = ((M + 255) / 256) * ((N + 255) / 256);
     if (K > 0 && M > 128 && wide_tiles >= 24) {
         const dbc_status c = mi::launch_wide(a, lda, b, ldb, p, st);
@@ -673,9 +680,11 @@ extern "C" dbc_status matmul_i8(const int8_t *a, int64_t lda, const float *a_sca
     // The split kernel's token tiles are the grid's second dimension (65535); only a depth of zero leaves
     // it more of them than 24.
     const int64_t most = 65535 * 128, nt = (N + 127) / 128;
-    // Tokens of a tile: as few as leave at most 74 tiles, so that short epilogues run side by side
-    // (300 x 300 x 128: 3.7 us against 5.1 with 128 tokens) and long weights are not read by many tiles
-    // (64 x 8192 x 8192: 12.5 us against 15.8 with at most 148).
+    // Tokens of a tile: as few as leave at most 74 tiles, so that short epilogues run side by side (us with at
+    // most 37, 74 and 148 tiles: 300 x 1536 x 512 7.8, 6.4 and 6.5; 200 x 1024 x 2048 8.3, 7.4 and 7.9) and
+    // long weights are not read by many tiles (64 x 8192 x 8192 12.4, 12.4 and 15.5; 64 x 4096 x 4096 9.5, 8.9
+    // and 10.0).  Where the weight is short and the depth long, 37 is a little ahead (61 x 1543 x 1531 5.9
+    // against 6.2, 128 x 1024 x 1024 5.9 against 6.5).
     int tile = 16;
     while (tile < 128 && tile < M && ((M + tile - 1) / tile) * nt > 74) tile *= 2;
     for (int64_t m0 = 0; m0 < M; m0 += most) {

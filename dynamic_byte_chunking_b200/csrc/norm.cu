@@ -13,13 +13,14 @@
 // backward pass, whose threads keep their columns' dw sums in registers, copies
 // ahead at every width.  Rows off the 16-byte grid are in norm_odd.cuh.
 //
-// Measured (us on the device, of a copy's time for the same bytes): 2.2 M x 256
-// bf16 with residual 684 (102 %), 262144 x 512 158 (104 %), 20000 x 4096 103
-// (98 %); the 8-bit form 154 (94 %) and 103 (86 %), where the arithmetic of the
-// codes shows (two issue slots of three are taken); backward 100000 x 512 65 (98 %),
-// 65536 x 256 26 (81 %, with the join of the dw lines), 32749 x 1536 with fp32
-// dy 86 (73 %: its 137 registers leave an SM 12 warps; fewer registers spill
-// (153 us), fewer columns per thread pay more barriers (100 us)).
+// Measured (us on the device, of a copy's time for the same bytes; all inputs
+// larger than L2): 2.2 M x 256 bf16 with residual 650 (107 %), 262144 x 512 159
+// (104 %), 20000 x 4096 104 (98 %); the 8-bit form 155 (94 %) and 104 (86 %),
+// where the arithmetic of the codes shows (two issue slots of three are taken);
+// backward 2.2 M x 256 521 (101 %), 100000 x 512 with ds 67 (95 %), 65536 x 256
+// with ds 26.7 (78 %, with the join of the dw lines), 32749 x 1536 with fp32 dy 90
+// (69 %: its 136 registers leave an SM 12 warps; fewer registers spill (153 us),
+// fewer columns per thread pay more barriers (100 us)).
 #include "norm.cuh"
 #include "norm_odd.cuh"
 
@@ -704,7 +705,8 @@ inline OddPlan odd_plan(int d, int nv, int in_bytes, int out_bytes) {
 }
 // Rows of a tile: whole passes of the teams, `budget` bytes of shared memory at `row_bytes` a row, and
 // not so many that SMs stay without a tile.  Four CTAs to an SM forward (100000 x 257: 78 us with 56 KB,
-// 85 with 28, 94 with 78), two backward (92 us with 91 KB, 117 with 30).
+// 85 with 28, 94 with 78), two backward, where the fp64 sums take their part of 112 KB (94 us; without those
+// sums 92 us with 91 KB, 117 with 30).
 inline int odd_tile_rows(int64_t N, int row_bytes, int teams, int budget) {
     return std::max(1, (int)std::min<int64_t>(budget / row_bytes, N / (kSms * 4)) / teams) * teams;
 }

@@ -7,7 +7,7 @@
 // aligned 16-byte pieces that cover it (asynchronous copies into shared memory
 // one row ahead, whole pieces back out, elements only at its two ends) and only
 // the arithmetic goes element by element, column j * W + t by thread t of the W
-// that share the row: 71 and 68 us, two fifths of the rate; what is left is the
+// that share the row: 68 and 63 us, two fifths of the rate; what is left is the
 // latency of the tiles' barriers and of the element-wise shared-memory accesses
 // between them.  Nothing outside the row is written, and nothing in front
 // of the array or behind the row is read.

@@ -85,7 +85,7 @@ def rms_norm_backward(dy: np.ndarray, s: np.ndarray, w, eps: float, ds):
 def backward_bounds(dy, s, w, eps, ds, T):
     """(bound of dx, bound of dw).  The mean is off by CHAIN roundings of its terms' magnitudes and rstd^2 by
     CHAIN more; the rest are OPS roundings of each term.  A column of dw is N products added in fp32 chains of
-    at most N / 148 + 64 additions."""
+    at most 16 additions, which fp64 sums join and one rounding follows."""
     rs = rstd_of(s, eps)
     xh = s * rs
     g = dy if w is None else dy * w
@@ -94,7 +94,7 @@ def backward_bounds(dy, s, w, eps, ds, T):
     b = mag * (2 * CHAIN + OPS) * U32 + np.abs(dx) * (ROUND[T] + U32) + TINY[T]
     if ds is not None:
         b = b + np.abs(ds) * U32
-    chain = dy.shape[0] / 148 + 64
+    chain = 16 + 1
     return b, np.abs(dy * xh).sum(0) * (CHAIN / 2 + OPS + chain) * U32 + TINY["f32"]
 
 
